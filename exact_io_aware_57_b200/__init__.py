@@ -10,6 +10,8 @@ _BINDING_NAMES = {
     "attn_naive_scratch_size", "attn_device_status", "attn_launch_count", "AttnError",
     "attn_fwd_splitkv", "attn_splitkv_num_splits", "attn_splitkv_workspace_size", "attn_merge_partials", "attn_bwd_varlen", "attn_fwd_dv",
     "attn_fwd_partial", "attn_bwd_dv", "attn_quantize_e4m3", "attn_fwd_fp8",
+    "attn_cache_append", "attn_fwd_tree", "attn_fwd_tree_workspace_size", "attn_cache_weights",
+    "attn_cache_weights_workspace_size", "attn_cache_evict",
 }
 
 

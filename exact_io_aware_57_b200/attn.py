@@ -61,6 +61,12 @@ EXPORTS = {
                              _VP]),
     "attn_naive_scratch_size": (_SZ, [_I, _I]),
     "attn_fwd_naive": (_I, [_VP, _VP, _VP, _VP, _FP, _VP, _SZ, _I, _I, _I, _I, _I, _I, _F, _I, _VP]),
+    "attn_cache_append": (_I, [_VP, _VP, _VP, _IP, _I, _IP, _IP, _I, _I, _I, _I, _I, _VP]),
+    "attn_fwd_tree_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "attn_fwd_tree": (_I, [_VP, _VP, _VP, _VP, _VP, _LL, _IP, _VP, _FP, _I, _I, _I, _I, _I, _F, _VP, _SZ, _I, _VP]),
+    "attn_cache_weights_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "attn_cache_weights": (_I, [_VP, _FP, _VP, _IP, _I, _IP, _FP, _FP, _I, _I, _I, _I, _I, _I, _F, _VP, _SZ, _I, _VP]),
+    "attn_cache_evict": (_I, [_VP, _FP, _I, _I, _I, _VP, _FP, _IP, _IP, _I, _I, _I, _I, _VP]),
     "attn_strerror": (ctypes.c_char_p, [_I]),
     "attn_device_status": (_I, [_VP]),
     "attn_launch_count": (_LL, [_I]),
@@ -388,6 +394,167 @@ def attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqle
                                 scale, int(bool(causal)), _dev(workspace, "workspace"),
                                 workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream)))
     return dq, dk, dv
+
+
+class KVCache(ctypes.Structure):
+    """attn_kv_cache of include/attn.h (device addresses and sizes)."""
+    _fields_ = [("k", _VP), ("v", _VP), ("block_table", _IP), ("lens", _IP), ("num_pages", _I), ("page_size", _I),
+                ("max_pages", _I)]
+
+
+def _like(t, name, dtype, shape, device):
+    """t as a device pointer once its dtype, shape (None: any extent) and device are as stated."""
+    if t.dtype != dtype:
+        raise AttnError(f"{name} must be {dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
+        raise AttnError(f"{name} must have shape {list(shape)}, has {list(t.shape)}")
+    if t.device != device:
+        raise AttnError(f"{name} is on {t.device}, not on {device}")
+    return _dev(t, name)
+
+
+def _cache(k, v, lens, block_table, B, Hkv, d, dtype, device, name="cache"):
+    c = KVCache()
+    c.k = _like(k, f"k_{name}", dtype, (None, None, Hkv, d), device)
+    c.v = None if v is None else _like(v, f"v_{name}", dtype, tuple(k.shape), device)
+    c.num_pages, c.page_size = k.shape[0], k.shape[1]
+    c.lens = None if lens is None else _like(lens, "cache_lens", torch.int32, (B,), device)
+    if block_table is not None:
+        c.block_table = _like(block_table, "block_table", torch.int32, (B, None), device)
+        c.max_pages = block_table.shape[1]
+    return c
+
+
+def _rows_args(rows, row_lens, B, n, device):
+    """Pointers and width of the optional row list and row counts."""
+    rp = None if rows is None else _like(rows, "rows", torch.int32, (B, None), device)
+    lp = None if row_lens is None else _like(row_lens, "row_lens", torch.int32, (B,), device)
+    return rp, n if rows is None else rows.shape[1], lp
+
+
+def _cache_stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def attn_cache_append(k_new, v_new, k_cache, v_cache, cache_lens, block_table=None, rows=None, row_lens=None,
+                      new_lens=None, stream=None):
+    """Write rows of k_new / v_new [B,T,Hkv,d] behind the last slot of each sequence of a
+    cache (k_cache / v_cache [pages, page_size, Hkv, d], cache_lens int32 [B], block_table
+    int32 [B, max_pages]; without a table page b is sequence b's): slot cache_lens[b] + i
+    takes row rows[b, i] (default i), i < row_lens[b] (default all).  Returns the new
+    lengths, int32 [B], in a buffer of their own; cache_lens is not changed."""
+    B, T, Hkv, d = k_new.shape
+    dev = k_new.device
+    c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, k_new.dtype, dev)
+    rp, width, lp = _rows_args(rows, row_lens, B, T, dev)
+    new_lens = torch.empty_like(cache_lens) if new_lens is None else new_lens
+    with torch.cuda.device(dev):
+        _check(_lib.attn_cache_append(_dev(k_new, "k_new"), _like(v_new, "v_new", k_new.dtype, k_new.shape, dev),
+                                      ctypes.byref(c), rp, width, lp,
+                                      _like(new_lens, "new_lens", torch.int32, (B,), dev), B, T, Hkv, d,
+                                      _dtype_code(k_new), _cache_stream(stream, dev)))
+    return new_lens
+
+
+def attn_fwd_tree_workspace_size(batch, h_q, h_kv, n_q, d, dtype=torch.bfloat16) -> int:
+    return int(_lib.attn_fwd_tree_workspace_size(batch, h_q, h_kv, n_q, d, ATTN_F32 if dtype == torch.float32 else
+                                                 ATTN_BF16))
+
+
+def attn_fwd_tree(q, k_cache, v_cache, cache_lens, k_new=None, v_new=None, block_table=None, tree_mask=None,
+                  row_lens=None, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """O, LSE of new tokens q [B,T,Hq,d] over a cache (see attn_cache_append) and their own
+    keys k_new / v_new [B,T,Hkv,d]: row t sees every cached slot and the new keys j with bit
+    j % 64 of tree_mask[(b,) t, j // 64] set (int64 [B,T,ceil(T/64)] or [T,ceil(T/64)];
+    default j <= t).  Without k_new the rows see the cache only.  Rows t >= row_lens[b] and
+    rows that see no key get O = 0, LSE = -inf.  T = 1 is a decode step."""
+    B, T, Hq, d = q.shape
+    Hkv = k_cache.shape[2]
+    dev = q.device
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, q.dtype, dev)
+    if (k_new is None) != (v_new is None):
+        raise AttnError("pass k_new and v_new together")
+    kp = None if k_new is None else _like(k_new, "k_new", q.dtype, (B, T, Hkv, d), dev)
+    vp = None if v_new is None else _like(v_new, "v_new", q.dtype, (B, T, Hkv, d), dev)
+    mp, mstride = None, 0
+    if tree_mask is not None:
+        words = (T + 63) // 64
+        per = tree_mask.dim() == 3
+        mp = _like(tree_mask, "tree_mask", torch.int64, (B, T, words) if per else (T, words), dev)
+        mstride = T * words if per else 0
+    _, _, lp = _rows_args(None, row_lens, B, T, dev)
+    o = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, Hq, T), device=dev, dtype=torch.float32) if lse is None else lse
+    if workspace is None:
+        workspace = torch.empty(attn_fwd_tree_workspace_size(B, Hq, Hkv, T, d, q.dtype), device=dev,
+                                dtype=torch.uint8)
+    with torch.cuda.device(dev):
+        _check(_lib.attn_fwd_tree(_dev(q, "q"), kp, vp, ctypes.byref(c), mp, mstride, lp,
+                                  _like(o, "out", q.dtype, q.shape, dev),
+                                  _like(lse, "lse", torch.float32, (B, Hq, T), dev), B, Hq, Hkv, T, d, scale,
+                                  _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                  _dtype_code(q), _cache_stream(stream, dev)))
+    return o, lse
+
+
+def attn_cache_weights_workspace_size(batch, h_q, h_kv, d, dtype=torch.bfloat16) -> int:
+    return int(_lib.attn_cache_weights_workspace_size(batch, h_q, h_kv, d, ATTN_F32 if dtype == torch.float32 else
+                                                      ATTN_BF16))
+
+
+def attn_cache_weights(q, lse, k_cache, cache_lens, weights, block_table=None, rows=None, row_lens=None, scale=None,
+                       out=None, workspace=None, stream=None):
+    """Add to weights fp32 [B,Hkv,cap] the attention weight each cached slot received from
+    the sequences' last tokens: the rows rows[b, i] (default i), i < row_lens[b] (default
+    all), of q [B,T,Hq,d] with their lse [B,Hq,T], each summed over the query heads of a
+    group; row i sees the slots j <= cache_lens[b] - count + i.  weights None: zeros, of
+    one page's or the table's capacity.  out: the result (default weights itself)."""
+    B, T, Hq, d = q.shape
+    Hkv = k_cache.shape[2]
+    dev = q.device
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    c = _cache(k_cache, None, cache_lens, block_table, B, Hkv, d, q.dtype, dev)
+    rp, width, lp = _rows_args(rows, row_lens, B, T, dev)
+    if out is None:
+        cap = c.page_size * (c.max_pages if block_table is not None else 1)
+        out = torch.empty((B, Hkv, cap), device=dev, dtype=torch.float32) if weights is None else weights
+    op = _like(out, "out", torch.float32, (B, Hkv, None), dev)
+    wp = None if weights is None else _like(weights, "weights", torch.float32, tuple(out.shape), dev)
+    if workspace is None:
+        workspace = torch.empty(attn_cache_weights_workspace_size(B, Hq, Hkv, d, q.dtype), device=dev,
+                                dtype=torch.uint8)
+    with torch.cuda.device(dev):
+        _check(_lib.attn_cache_weights(_dev(q, "q"), _like(lse, "lse", torch.float32, (B, Hq, T), dev),
+                                       ctypes.byref(c), rp, width, lp, wp, op, out.shape[2], B, Hq, Hkv, T, d, scale,
+                                       _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                       _dtype_code(q), _cache_stream(stream, dev)))
+    return out
+
+
+def attn_cache_evict(k_cache, v_cache, weights, cache_lens, keep, k_out, v_out, recent=0, block_table=None,
+                     out_table=None, weights_out=None, kept=None, new_lens=None, stream=None):
+    """Cut each sequence of a cache down to keep slots, per KV head: the last `recent` slots
+    and the others of largest weight (fp32 [B,Hkv,cap]; ties: the lower slot).  They go in
+    ascending order to the cache k_out / v_out (out_table), whose pages are others than the
+    source's.  Returns weights_out (like weights, zeros behind the last slot), kept int32
+    [B,Hkv,keep] (source slots, -1 behind the last) and new_lens int32 [B]."""
+    Hkv, d = k_cache.shape[2], k_cache.shape[3]
+    B, dev = weights.shape[0], k_cache.device
+    keep, recent = int(keep), int(recent)
+    src = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, k_cache.dtype, dev)
+    dst = _cache(k_out, v_out, None, out_table, B, Hkv, d, k_cache.dtype, dev, name="out")
+    wp = _like(weights, "weights", torch.float32, (B, Hkv, None), dev)
+    weights_out = torch.empty_like(weights) if weights_out is None else weights_out
+    kept = torch.empty((B, Hkv, max(keep, 0)), device=dev, dtype=torch.int32) if kept is None else kept
+    new_lens = torch.empty_like(cache_lens) if new_lens is None else new_lens
+    with torch.cuda.device(dev):
+        _check(_lib.attn_cache_evict(ctypes.byref(src), wp, weights.shape[2], keep, recent, ctypes.byref(dst),
+                                     _like(weights_out, "weights_out", torch.float32, tuple(weights.shape), dev),
+                                     _like(kept, "kept", torch.int32, (B, Hkv, keep), dev),
+                                     _like(new_lens, "new_lens", torch.int32, (B,), dev), B, Hkv, d,
+                                     _dtype_code(k_cache), _cache_stream(stream, dev)))
+    return weights_out, kept, new_lens
 
 
 def attn_naive_scratch_size(n_q, n_k) -> int:

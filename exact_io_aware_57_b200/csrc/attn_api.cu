@@ -27,6 +27,9 @@ EncodeTiledFn g_encode = nullptr;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+}  // namespace
+
 bool supported_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
@@ -34,9 +37,6 @@ bool supported_device() {
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return false;
   return major == 10;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-}  // namespace
 
 void count_launch(int n) { g_launches += n; }
 

@@ -1,0 +1,223 @@
+// Tree attention and accumulated key weights over a cache on the CUDA cores:
+// the fp32 path.
+//
+// Tree attention.  A block owns 8 query rows (row = (drafted token t, head g of
+// the group), one per warp) of one (sequence, KV head) and walks every
+// num_splits-th 32-key tile of the cached slots and then of the drafted keys:
+// K and V tiles in shared memory, lane = key for the scores, lane = column
+// group for P V, the running softmax state (m, l, a) in registers ("Softmax
+// does not need the matrix", "Carry the Normalizer").  The splits' partials are
+// merged by merge.cu.  Splitting strides over tiles, so that splits of ragged
+// sequences stay level without the host knowing a length.
+//
+// Key weights.  A block owns 32 slots of one (sequence, KV head): lane = slot,
+// the warps share out the counted (row, head) pairs, and their sums are added
+// in warp order.
+#include <algorithm>
+
+#include "cache.cuh"
+#include "kernels.h"
+
+namespace attn {
+namespace {
+
+constexpr int KT = 32;    // keys per tile
+constexpr int ROWS = 8;   // query rows (warps) per block
+
+template <typename T>
+ATTN_DEVINL float4 load4(const T* p);
+template <>
+ATTN_DEVINL float4 load4<float>(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <>
+ATTN_DEVINL float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+ATTN_DEVINL float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+ATTN_DEVINL float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * ROWS) tree_simt_kernel(TreeParams p) {
+  constexpr int S = D + 4;  // padded row: 16-byte reads of 8 consecutive rows hit distinct banks
+  constexpr int E = D / 32;
+  __shared__ float ks[KT * S], vs[KT * S], qs[ROWS * D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv;
+  const int b = blockIdx.z, split = blockIdx.y % p.num_splits, hk = blockIdx.y / p.num_splits;
+  const int r = blockIdx.x * ROWS + warp;  // row (t, g) of the group
+  const int t = r / G, h = hk * G + r % G;
+  int len, nr;
+  if (!cache_len(p.c, b, 1ll << 31, p.status, len) || !row_count(p.row_lens, b, p.Nq, p.status, nr)) len = nr = 0;
+  const bool valid = t < p.Nq;
+  const bool row_ok = t < nr;
+  const int n_new = p.k_new ? nr : 0;
+  const T* q = static_cast<const T*>(p.q) + (((long long)b * p.Nq + (valid ? t : 0)) * p.Hq + h) * D;
+  for (int c = lane; c < D / 4; c += 32)
+    *reinterpret_cast<float4*>(&qs[warp * D + 4 * c]) = load4<T>(q + 4 * c);
+  const unsigned long long* mrow =
+      p.mask && valid ? p.mask + (long long)b * p.mask_bstride + (long long)t * p.mask_words : nullptr;
+
+  float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const int tiles_c = (len + KT - 1) / KT, tiles = tiles_c + (n_new + KT - 1) / KT;
+  for (int tile = split; tile < tiles; tile += p.num_splits) {
+    const bool cached = tile < tiles_c;
+    const int base = (cached ? tile : tile - tiles_c) * KT;
+    const int n = min(KT, (cached ? len : n_new) - base);
+    __syncthreads();
+    for (int i = threadIdx.x; i < KT * (D / 4); i += 32 * ROWS) {
+      const int key = i / (D / 4), c = 4 * (i % (D / 4));
+      float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
+      if (key < n) {
+        const long long row = cached ? cache_row(p.c, b, base + key, p.status) : (long long)b * p.Nq + base + key;
+        if (row >= 0) {
+          const long long at = (row * p.Hkv + hk) * D + c;
+          kk = load4<T>(static_cast<const T*>(cached ? p.c.k : p.k_new) + at);
+          vv = load4<T>(static_cast<const T*>(cached ? p.c.v : p.v_new) + at);
+        }
+      }
+      *reinterpret_cast<float4*>(&ks[key * S + c]) = kk;
+      *reinterpret_cast<float4*>(&vs[key * S + c]) = vv;
+    }
+    __syncthreads();
+    if (!row_ok) continue;
+    float s = 0.f;
+#pragma unroll 8
+    for (int c = 0; c < D; c += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(&qs[warp * D + c]);
+      const float4 k = *reinterpret_cast<const float4*>(&ks[lane * S + c]);
+      s = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, s))));
+    }
+    bool see = lane < n;
+    if (see && !cached) {
+      const int j = base + lane;
+      see = mrow ? (mrow[j >> 6] >> (j & 63)) & 1 : j <= t;
+    }
+    s = see ? s * p.scale : -INFINITY;
+    const float m_new = fmaxf(m, warp_max(s));
+    if (m_new == -INFINITY) continue;
+    const float alpha = expf(m - m_new), w = see ? expf(s - m_new) : 0.f;
+    l = l * alpha + warp_sum(w);
+    m = m_new;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= alpha;
+    // only seen keys enter the sum: a hidden key's V may hold anything
+    for (unsigned live = __ballot_sync(0xffffffffu, see); live; live &= live - 1) {
+      const int j = __ffs(live) - 1;
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(wj, vs[j * S + lane * E + e], acc[e]);
+    }
+  }
+  if (!valid) return;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const long long at = (long long)b * p.Nq + t;
+  float* o = p.o_part + ((long long)split * p.B * p.Nq + at) * p.Hq * D + (long long)h * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = acc[e] * inv;
+  if (lane == 0)
+    p.lse_part[(((long long)split * p.B + b) * p.Hq + h) * p.Nq + t] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * ROWS) weights_simt_kernel(WeightsParams p) {
+  constexpr int S = D + 4;
+  __shared__ float ks[KT * S], part[ROWS][KT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv, hk = blockIdx.y, b = blockIdx.z, base = blockIdx.x * KT;
+  int len, nr;
+  if (!cache_len(p.c, b, p.cap, p.status, len) || !row_count(p.row_lens, b, p.max_rows, p.status, nr)) return;
+  const int n = min(KT, len - base);  // slots of this tile in use (may be negative)
+  for (int i = threadIdx.x; i < KT * (D / 4); i += 32 * ROWS) {
+    const int key = i / (D / 4), c = 4 * (i % (D / 4));
+    float4 kk = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (key < n) {
+      const long long row = cache_row(p.c, b, base + key, p.status);
+      if (row >= 0) kk = load4<T>(static_cast<const T*>(p.c.k) + (row * p.Hkv + hk) * D + c);
+    }
+    *reinterpret_cast<float4*>(&ks[key * S + c]) = kk;
+  }
+  __syncthreads();
+  float acc = 0.f;
+  if (n > 0) {
+    const int first = max(0, base - (len - nr));  // earlier rows see no slot of this tile
+    for (int i = first * G + warp; i < nr * G; i += ROWS) {
+      const int row = i / G, h = hk * G + i % G;
+      const int t = p.rows ? p.rows[(long long)b * p.max_rows + row] : row;
+      if (t < 0 || t >= p.Nq) {
+        if (lane == 0) atomicExch(p.status, ATTN_ERR_INVALID);
+        continue;
+      }
+      const T* q = static_cast<const T*>(p.q) + (((long long)b * p.Nq + t) * p.Hq + h) * D;
+      const float z = p.lse[((long long)b * p.Hq + h) * p.Nq + t];
+      float s = 0.f;
+#pragma unroll 8
+      for (int c = 0; c < D; c += 4) {
+        const float4 a = load4<T>(q + c);
+        const float4 k = *reinterpret_cast<const float4*>(&ks[lane * S + c]);
+        s = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, s))));
+      }
+      // a row without a visible key (LSE = -inf) weighs nothing
+      if (lane < n && base + lane <= len - nr + row && z != -INFINITY) acc += expf(s * p.scale - z);
+    }
+  }
+  part[warp][lane] = acc;
+  __syncthreads();
+  const int j = base + lane;
+  if (warp == 0 && j < p.cap) {
+    const long long at = ((long long)b * p.Hkv + hk) * p.cap + j;
+    float w = p.weights ? p.weights[at] : 0.f, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) sum += part[i][lane];
+    if (lane < n) w += sum;
+    p.out[at] = w;
+  }
+}
+
+}  // namespace
+
+// Splits of the keys such that about two blocks land on each SM.
+int tree_simt_splits(int B, int Hq, int Hkv, int Nq, long long capacity) {
+  const long long blocks = (long long)B * Hkv * (((long long)Nq * (Hq / Hkv) + ROWS - 1) / ROWS);
+  const long long tiles = (capacity + Nq + KT - 1) / KT;
+  const long long want = std::min((4ll * sm_count() + blocks - 1) / blocks, 65535ll / Hkv);
+  return (int)std::max(1ll, std::min(std::min(want, tiles), 64ll));
+}
+
+int launch_tree_simt(const TreeParams& p, cudaStream_t st) {
+  const int G = p.Hq / p.Hkv;
+  const dim3 grid((unsigned)(((long long)p.Nq * G + ROWS - 1) / ROWS), (unsigned)(p.Hkv * p.num_splits), (unsigned)p.B);
+  if (p.bf16)
+    (p.D == 64 ? tree_simt_kernel<__nv_bfloat16, 64> : tree_simt_kernel<__nv_bfloat16, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
+  else
+    (p.D == 64 ? tree_simt_kernel<float, 64> : tree_simt_kernel<float, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
+  count_launch();
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  return launch_merge(p.o_part, p.lse_part, p.num_splits, p.o, p.lse, p.B, p.Hq, p.Nq, p.D, !p.bf16, st);
+}
+
+int launch_weights_simt(const WeightsParams& p, cudaStream_t st) {
+  const dim3 grid((unsigned)((p.cap + KT - 1) / KT), (unsigned)p.Hkv, (unsigned)p.B);
+  if (p.bf16)
+    (p.D == 64 ? weights_simt_kernel<__nv_bfloat16, 64> : weights_simt_kernel<__nv_bfloat16, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
+  else
+    (p.D == 64 ? weights_simt_kernel<float, 64> : weights_simt_kernel<float, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
+  count_launch();
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace attn

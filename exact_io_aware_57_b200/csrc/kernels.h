@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/attn.h"
+#include "cache.cuh"
 
 namespace attn {
 
@@ -21,6 +22,8 @@ constexpr long long kWaitLimitCycles = 2000000000LL;
 
 // Device address of the library's status word on the current device.
 int* device_status_ptr();
+// Whether the current device is one these kernels are built for.
+bool supported_device();
 // Streaming multiprocessors of the current device (1 if the query fails).
 int sm_count();
 
@@ -155,6 +158,66 @@ int launch_fwd_naive(const TcGeom& g, __nv_bfloat16* o, float* lse, float* s_scr
 // limit_cycles (the shared bounded-wait failure path).
 int launch_wait_selftest(long long limit_cycles, cudaStream_t st);
 int launch_ex2_selftest(const float* x, float* y, long long n, cudaStream_t st);
+
+// ------------------------------------------------- key/value cache (cache.cuh)
+// Tree attention: row t of sequence b sees its cached slots and the drafted
+// keys j with bit j of its mask row (without a mask: j <= t).
+struct TreeParams {
+  const void *q, *k_new, *v_new;  // k_new / v_new null: no drafted keys
+  CacheView c;
+  const unsigned long long* mask;  // [mask_words] per row, or null
+  long long mask_bstride;          // words; 0: one mask for every sequence
+  int mask_words;
+  const int* row_lens;
+  void* o;
+  float* lse;
+  int B, Hq, Hkv, Nq, D, bf16;
+  float scale;
+  int num_splits;
+  float *o_part, *lse_part;  // as SplitKV's
+  int* status;
+};
+int tree_simt_splits(int B, int Hq, int Hkv, int Nq, long long capacity);
+int launch_tree_simt(const TreeParams& p, cudaStream_t st);
+
+// out[b, hk, j] = weights[b, hk, j] + sum over counted rows i and the heads of
+// the group of exp(scale q . k_j - lse), j <= len - count + i.
+struct WeightsParams {
+  const void* q;
+  const float* lse;
+  CacheView c;
+  const int *rows, *row_lens;
+  int max_rows;
+  const float* weights;  // null: zeros
+  float* out;
+  int cap;  // slots per (sequence, KV head) of weights and out
+  int B, Hq, Hkv, Nq, D, bf16;
+  float scale;
+  int* status;
+};
+int launch_weights_simt(const WeightsParams& p, cudaStream_t st);
+
+struct AppendParams {
+  const void *k_new, *v_new;  // rows of row_bytes, n_new per sequence
+  CacheView c;
+  const int *rows, *row_lens;
+  int max_rows, n_new, B, row_bytes;
+  int* new_lens;
+  int* status;
+};
+int launch_append(const AppendParams& p, cudaStream_t st);
+
+struct EvictParams {
+  CacheView src, dst;  // dst.lens unused
+  const float* weights;
+  float* weights_out;
+  int cap;  // slots per (sequence, KV head) of weights and weights_out
+  int keep, recent;
+  int *kept, *new_lens;  // [B, Hkv, keep], [B]
+  int B, Hkv, head_bytes;
+  int* status;
+};
+int launch_evict(const EvictParams& p, cudaStream_t st);
 
 // Tensor-map encoding (driver entry point resolved at run time).
 int encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,

@@ -289,6 +289,119 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float*
                     int h_kv, int d, float scale, int causal, int dtype, void* stream);
 
 /*
+ * ---- Key/value cache ----------------------------------------------------
+ *
+ * A cache holds the key and value rows of `batch` sequences in pages of
+ * page_size rows: k, v are DEVICE [num_pages, page_size, h_kv, d] (16-byte
+ * aligned), and slot s of sequence b is row s % page_size of page
+ * block_table[b * max_pages + s / page_size].  With block_table NULL page b
+ * belongs to sequence b (num_pages >= batch; max_pages is ignored, page_size
+ * may be any size); with a table page_size must be a multiple of 8.  lens[b],
+ * DEVICE int32, is the number of slots of sequence b in use.
+ *
+ * lens, block_table, row_lens and rows are DEVICE int32 and are never read on
+ * the host, so that a step can be captured into a graph and replayed as the
+ * cache grows.  The kernels check them: a length outside [0, slots the table
+ * can name], a count outside its bound, a row index outside the given rows, or
+ * a page number outside [0, num_pages) raises ATTN_ERR_INVALID in the device
+ * status word (attn_device_status).  Nothing outside the buffers is touched,
+ * other sequences are computed as ever, and what such a sequence gets is
+ * stated with each call; behind a page number out of range its result is
+ * undefined.  Rows behind lens[b] are never used, whatever they hold.
+ *
+ * Both dtypes are taken everywhere; at most 65535 heads or batch elements and
+ * 2^28 slots per sequence.
+ */
+typedef struct attn_kv_cache {
+  void* k;
+  void* v;
+  const int* block_table;
+  const int* lens;
+  int num_pages;
+  int page_size;
+  int max_pages;
+} attn_kv_cache;
+
+/*
+ * Write new rows behind each sequence's last slot: slot lens[b] + i takes row
+ * rows[b * max_rows + i] (rows NULL: row i, max_rows <= n_new) of k_new, v_new
+ * [batch, n_new, h_kv, d], for i < row_lens[b] (NULL: max_rows).  new_lens[b]
+ * = lens[b] + row_lens[b]; new_lens is another buffer than lens.  With the
+ * accepted path of a verified tree as `rows` only accepted rows enter the
+ * cache.  The table must name pages for the new slots.  A sequence whose
+ * length or count is not acceptable, or whose rows do not fit, is left as it is.
+ */
+int attn_cache_append(const void* k_new, const void* v_new, const attn_kv_cache* cache,
+                      const int* rows, int max_rows, const int* row_lens, int* new_lens, int batch,
+                      int n_new, int h_kv, int d, int dtype, void* stream);
+
+/*
+ * Attention of a few new tokens over a cache: one token per sequence (a decode
+ * step), a chunk, or a tree of drafted tokens.  Row t < row_lens[b] (NULL:
+ * n_q) of q [batch, n_q, h_q, d] sees every cached slot of its sequence and,
+ * of the new keys k_new, v_new [batch, n_q, h_kv, d], those j < row_lens[b]
+ * with bit j % 64 of word j / 64 of its mask row set:
+ *   tree_mask: DEVICE 64-bit words [batch, n_q, ceil(n_q / 64)], sequences
+ *   mask_batch_stride words apart (0: one mask for all); NULL: j <= t.
+ * k_new and v_new may both be NULL: the rows see the cache only.  The new keys
+ * are not written to the cache; attn_cache_append does that.
+ * o [batch, n_q, h_q, d] like q, lse fp32 [batch, h_q, n_q] as attn_fwd; rows
+ * that see no key, and the rows t >= row_lens[b], get O = 0, LSE = -inf, and so
+ * do all rows of a sequence whose length or count is not acceptable.
+ * The value rows of cached slots and of new keys j < row_lens[b] take part in
+ * matrix products with P = 0 where a row does not see them: they must be finite.
+ * n_q <= 4096.  workspace: DEVICE, 256-byte aligned,
+ * attn_fwd_tree_workspace_size(...) bytes, contents need not be initialised;
+ * calls that may overlap on the device need one each.
+ */
+size_t attn_fwd_tree_workspace_size(int batch, int h_q, int h_kv, int n_q, int d, int dtype);
+int attn_fwd_tree(const void* q, const void* k_new, const void* v_new, const attn_kv_cache* cache,
+                  const long long* tree_mask, long long mask_batch_stride, const int* row_lens,
+                  void* o, float* lse, int batch, int h_q, int h_kv, int n_q, int d, float scale,
+                  void* workspace, size_t workspace_bytes, int dtype, void* stream);
+
+/*
+ * Accumulate the attention weight that each cached slot receives.  The counted
+ * rows of sequence b are rows[b * max_rows + i] (rows NULL: i, max_rows <= n_q)
+ * of q, i < count = row_lens[b] (NULL: max_rows); they are the sequence's last
+ * tokens, already in the cache, so row i sees the slots j <= lens[b] - count + i:
+ *   out[b, hk, j] = weights[b, hk, j]
+ *     + sum over counted rows i that see j and heads h of group hk of
+ *       exp(scale * q[b, row_i, h] . k_j - lse[b, h, row_i]),
+ * in fp32, with lse [batch, h_q, n_q] as the attention over those slots
+ * returned it (a row with LSE = -inf adds nothing).  weights, out: DEVICE fp32
+ * [batch, h_kv, cap], cap >= lens[b]; weights NULL means zeros; out may be
+ * weights.  Slots j >= lens[b] take weights' value.  The V rows are not used:
+ * cache->v may be NULL.  A prompt is the case lens[b] = count = n_q.
+ * A sequence whose length or count is not acceptable is left as it is in out.
+ * workspace: as attn_fwd_tree's, attn_cache_weights_workspace_size(...) bytes.
+ */
+size_t attn_cache_weights_workspace_size(int batch, int h_q, int h_kv, int d, int dtype);
+int attn_cache_weights(const void* q, const float* lse, const attn_kv_cache* cache, const int* rows,
+                       int max_rows, const int* row_lens, const float* weights, float* out, int cap,
+                       int batch, int h_q, int h_kv, int n_q, int d, float scale, void* workspace,
+                       size_t workspace_bytes, int dtype, void* stream);
+
+/*
+ * Cut each sequence down to `keep` slots, for each KV head by itself.  When
+ * lens[b] > keep the last `recent` slots stay, and of the others the keep -
+ * recent of largest weight (equal weights: the lower slot first; a NaN weight
+ * counts as -inf); otherwise every slot stays.  The slots that stay go, in
+ * ascending order, to slots 0, 1, ... of `dst` (dst->lens is not used), whose
+ * pages must be others than the source's, with their weights:
+ *   kept[b, hk, i]  = source slot of slot i of head hk, -1 behind the last one;
+ *   weights_out[b, hk, i] = weights[b, hk, kept], 0 behind the last one;
+ *   new_lens[b] = min(lens[b], keep).
+ * weights, weights_out: DEVICE fp32 [batch, h_kv, cap], cap >= lens[b] (two
+ * buffers); kept: DEVICE int32 [batch, h_kv, keep]; 0 <= recent <= keep.  A
+ * sequence whose length is not acceptable, or does not fit dst, gets kept = -1
+ * and new_lens[b] = lens[b], and nothing else is written for it.
+ */
+int attn_cache_evict(const attn_kv_cache* cache, const float* weights, int cap, int keep, int recent,
+                     const attn_kv_cache* dst, float* weights_out, int* kept, int* new_lens,
+                     int batch, int h_kv, int d, int dtype, void* stream);
+
+/*
  * Deliberately naive materialising forward, for measurement only (the
  * three-step "standard attention" the pages contrast with: write S to device
  * memory, read it back for the row softmax and write P, read P for P V).
