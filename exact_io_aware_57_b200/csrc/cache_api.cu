@@ -87,6 +87,7 @@ int attn_cache_append(const void* k_new, const void* v_new, const attn_kv_cache*
 
 size_t attn_fwd_tree_workspace_size(int batch, int h_q, int h_kv, int n_q, int d, int dtype) {
   if (check_sizes(batch, h_q, h_kv, d, dtype) || n_q <= 0) return 0;
+  if (dtype == ATTN_BF16) return tree_sm100_workspace(h_q, h_kv, n_q, d);
   const int splits = tree_simt_splits(batch, h_q, h_kv, n_q, kMaxSeqLen);
   return partial_bytes(splits, batch, h_q, n_q, d);
 }
@@ -123,6 +124,10 @@ int attn_fwd_tree(const void* q, const void* k_new, const void* v_new, const att
   p.bf16 = dtype == ATTN_BF16;
   p.scale = scale;
   if (!(p.status = device_status_ptr())) return ATTN_ERR_CUDA;
+  if (dtype == ATTN_BF16) {
+    if (workspace_bytes < tree_sm100_workspace(h_q, h_kv, n_q, d)) return ATTN_ERR_WORKSPACE;
+    return launch_tree_sm100(p, workspace, static_cast<cudaStream_t>(stream));
+  }
   p.num_splits = tree_simt_splits(batch, h_q, h_kv, n_q, capacity_of(p.c));
   if (workspace_bytes < partial_bytes(p.num_splits, batch, h_q, n_q, d)) return ATTN_ERR_WORKSPACE;
   p.o_part = static_cast<float*>(workspace);

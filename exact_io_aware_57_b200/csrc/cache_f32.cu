@@ -201,13 +201,10 @@ int tree_simt_splits(int B, int Hq, int Hkv, int Nq, long long capacity) {
 int launch_tree_simt(const TreeParams& p, cudaStream_t st) {
   const int G = p.Hq / p.Hkv;
   const dim3 grid((unsigned)(((long long)p.Nq * G + ROWS - 1) / ROWS), (unsigned)(p.Hkv * p.num_splits), (unsigned)p.B);
-  if (p.bf16)
-    (p.D == 64 ? tree_simt_kernel<__nv_bfloat16, 64> : tree_simt_kernel<__nv_bfloat16, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
-  else
-    (p.D == 64 ? tree_simt_kernel<float, 64> : tree_simt_kernel<float, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
+  (p.D == 64 ? tree_simt_kernel<float, 64> : tree_simt_kernel<float, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
   count_launch();
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  return launch_merge(p.o_part, p.lse_part, p.num_splits, p.o, p.lse, p.B, p.Hq, p.Nq, p.D, !p.bf16, st);
+  return launch_merge(p.o_part, p.lse_part, p.num_splits, p.o, p.lse, p.B, p.Hq, p.Nq, p.D, 1, st);
 }
 
 int launch_weights_simt(const WeightsParams& p, cudaStream_t st) {

@@ -162,6 +162,11 @@ int launch_ex2_selftest(const float* x, float* y, long long n, cudaStream_t st);
 // ------------------------------------------------- key/value cache (cache.cuh)
 // Tree attention: row t of sequence b sees its cached slots and the drafted
 // keys j with bit j of its mask row (without a mask: j <= t).
+// pair2 = 2 * pair + (two row tiles); `more` later parts follow the first one
+// (0: the CTA's run begins no unit that a cut divides).
+struct TreeCut {
+  int b, hk, pair2, more;
+};
 struct TreeParams {
   const void *q, *k_new, *v_new;  // k_new / v_new null: no drafted keys
   CacheView c;
@@ -174,9 +179,14 @@ struct TreeParams {
   int B, Hq, Hkv, Nq, D, bf16;
   float scale;
   int num_splits;
-  float *o_part, *lse_part;  // as SplitKV's
+  float *o_part, *lse_part;  // fp32 path: as SplitKV's; bf16 path: raw O, and (m, l) pairs
+  int part_tiles;            // bf16 path: row tiles of a partial (1 or 2)
+  TreeCut* cuts;             // one per CTA
   int* status;
+  long long wait_limit;
 };
+size_t tree_sm100_workspace(int Hq, int Hkv, int Nq, int D);
+int launch_tree_sm100(TreeParams p, void* workspace, cudaStream_t st);
 int tree_simt_splits(int B, int Hq, int Hkv, int Nq, long long capacity);
 int launch_tree_simt(const TreeParams& p, cudaStream_t st);
 
