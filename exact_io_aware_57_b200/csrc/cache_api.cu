@@ -88,7 +88,7 @@ int attn_cache_append(const void* k_new, const void* v_new, const attn_kv_cache*
 size_t attn_fwd_tree_workspace_size(int batch, int h_q, int h_kv, int n_q, int d, int dtype) {
   if (check_sizes(batch, h_q, h_kv, d, dtype) || n_q <= 0) return 0;
   if (dtype == ATTN_BF16) return tree_sm100_workspace(h_q, h_kv, n_q, d);
-  const int splits = tree_simt_splits(batch, h_q, h_kv, n_q, kMaxSeqLen);
+  const int splits = tree_f32_splits(batch, h_q, h_kv, n_q, kMaxSeqLen);
   return partial_bytes(splits, batch, h_q, n_q, d);
 }
 
@@ -121,24 +121,23 @@ int attn_fwd_tree(const void* q, const void* k_new, const void* v_new, const att
   p.Hkv = h_kv;
   p.Nq = n_q;
   p.D = d;
-  p.bf16 = dtype == ATTN_BF16;
   p.scale = scale;
   if (!(p.status = device_status_ptr())) return ATTN_ERR_CUDA;
   if (dtype == ATTN_BF16) {
     if (workspace_bytes < tree_sm100_workspace(h_q, h_kv, n_q, d)) return ATTN_ERR_WORKSPACE;
     return launch_tree_sm100(p, workspace, static_cast<cudaStream_t>(stream));
   }
-  p.num_splits = tree_simt_splits(batch, h_q, h_kv, n_q, capacity_of(p.c));
+  p.num_splits = tree_f32_splits(batch, h_q, h_kv, n_q, capacity_of(p.c));
   if (workspace_bytes < partial_bytes(p.num_splits, batch, h_q, n_q, d)) return ATTN_ERR_WORKSPACE;
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                         align256((size_t)p.num_splits * batch * n_q * h_q * d * sizeof(float)));
-  return launch_tree_simt(p, static_cast<cudaStream_t>(stream));
+  return launch_tree_f32(p, static_cast<cudaStream_t>(stream));
 }
 
 size_t attn_cache_weights_workspace_size(int batch, int h_q, int h_kv, int d, int dtype) {
   if (check_sizes(batch, h_q, h_kv, d, dtype)) return 0;
-  return 256;
+  return dtype == ATTN_BF16 ? weights_sm100_workspace() : 256;
 }
 
 int attn_cache_weights(const void* q, const float* lse, const attn_kv_cache* cache, const int* rows, int max_rows,
@@ -169,10 +168,10 @@ int attn_cache_weights(const void* q, const float* lse, const attn_kv_cache* cac
   p.Hkv = h_kv;
   p.Nq = n_q;
   p.D = d;
-  p.bf16 = dtype == ATTN_BF16;
   p.scale = scale;
   if (!(p.status = device_status_ptr())) return ATTN_ERR_CUDA;
-  return launch_weights_simt(p, static_cast<cudaStream_t>(stream));
+  if (dtype == ATTN_BF16) return launch_weights_sm100(p, workspace, static_cast<cudaStream_t>(stream));
+  return launch_weights_f32(p, static_cast<cudaStream_t>(stream));
 }
 
 int attn_cache_evict(const attn_kv_cache* cache, const float* weights, int cap, int keep, int recent,

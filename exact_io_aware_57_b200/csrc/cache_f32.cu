@@ -24,19 +24,7 @@ namespace {
 constexpr int KT = 32;    // keys per tile
 constexpr int ROWS = 8;   // query rows (warps) per block
 
-template <typename T>
-ATTN_DEVINL float4 load4(const T* p);
-template <>
-ATTN_DEVINL float4 load4<float>(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-ATTN_DEVINL float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
+ATTN_DEVINL float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
 ATTN_DEVINL float warp_max(float x) {
 #pragma unroll
@@ -49,8 +37,8 @@ ATTN_DEVINL float warp_sum(float x) {
   return x;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * ROWS) tree_simt_kernel(TreeParams p) {
+template <int D>
+__global__ void __launch_bounds__(32 * ROWS) tree_f32_kernel(TreeParams p) {
   constexpr int S = D + 4;  // padded row: 16-byte reads of 8 consecutive rows hit distinct banks
   constexpr int E = D / 32;
   __shared__ float ks[KT * S], vs[KT * S], qs[ROWS * D];
@@ -64,9 +52,9 @@ __global__ void __launch_bounds__(32 * ROWS) tree_simt_kernel(TreeParams p) {
   const bool valid = t < p.Nq;
   const bool row_ok = t < nr;
   const int n_new = p.k_new ? nr : 0;
-  const T* q = static_cast<const T*>(p.q) + (((long long)b * p.Nq + (valid ? t : 0)) * p.Hq + h) * D;
+  const float* q = static_cast<const float*>(p.q) + (((long long)b * p.Nq + (valid ? t : 0)) * p.Hq + h) * D;
   for (int c = lane; c < D / 4; c += 32)
-    *reinterpret_cast<float4*>(&qs[warp * D + 4 * c]) = load4<T>(q + 4 * c);
+    *reinterpret_cast<float4*>(&qs[warp * D + 4 * c]) = load4(q + 4 * c);
   const unsigned long long* mrow =
       p.mask && valid ? p.mask + (long long)b * p.mask_bstride + (long long)t * p.mask_words : nullptr;
 
@@ -86,8 +74,8 @@ __global__ void __launch_bounds__(32 * ROWS) tree_simt_kernel(TreeParams p) {
         const long long row = cached ? cache_row(p.c, b, base + key, p.status) : (long long)b * p.Nq + base + key;
         if (row >= 0) {
           const long long at = (row * p.Hkv + hk) * D + c;
-          kk = load4<T>(static_cast<const T*>(cached ? p.c.k : p.k_new) + at);
-          vv = load4<T>(static_cast<const T*>(cached ? p.c.v : p.v_new) + at);
+          kk = load4(static_cast<const float*>(cached ? p.c.k : p.k_new) + at);
+          vv = load4(static_cast<const float*>(cached ? p.c.v : p.v_new) + at);
         }
       }
       *reinterpret_cast<float4*>(&ks[key * S + c]) = kk;
@@ -133,8 +121,8 @@ __global__ void __launch_bounds__(32 * ROWS) tree_simt_kernel(TreeParams p) {
     p.lse_part[(((long long)split * p.B + b) * p.Hq + h) * p.Nq + t] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * ROWS) weights_simt_kernel(WeightsParams p) {
+template <int D>
+__global__ void __launch_bounds__(32 * ROWS) weights_f32_kernel(WeightsParams p) {
   constexpr int S = D + 4;
   __shared__ float ks[KT * S], part[ROWS][KT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -147,7 +135,7 @@ __global__ void __launch_bounds__(32 * ROWS) weights_simt_kernel(WeightsParams p
     float4 kk = make_float4(0.f, 0.f, 0.f, 0.f);
     if (key < n) {
       const long long row = cache_row(p.c, b, base + key, p.status);
-      if (row >= 0) kk = load4<T>(static_cast<const T*>(p.c.k) + (row * p.Hkv + hk) * D + c);
+      if (row >= 0) kk = load4(static_cast<const float*>(p.c.k) + (row * p.Hkv + hk) * D + c);
     }
     *reinterpret_cast<float4*>(&ks[key * S + c]) = kk;
   }
@@ -162,12 +150,12 @@ __global__ void __launch_bounds__(32 * ROWS) weights_simt_kernel(WeightsParams p
         if (lane == 0) atomicExch(p.status, ATTN_ERR_INVALID);
         continue;
       }
-      const T* q = static_cast<const T*>(p.q) + (((long long)b * p.Nq + t) * p.Hq + h) * D;
+      const float* q = static_cast<const float*>(p.q) + (((long long)b * p.Nq + t) * p.Hq + h) * D;
       const float z = p.lse[((long long)b * p.Hq + h) * p.Nq + t];
       float s = 0.f;
 #pragma unroll 8
       for (int c = 0; c < D; c += 4) {
-        const float4 a = load4<T>(q + c);
+        const float4 a = load4(q + c);
         const float4 k = *reinterpret_cast<const float4*>(&ks[lane * S + c]);
         s = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, s))));
       }
@@ -191,28 +179,25 @@ __global__ void __launch_bounds__(32 * ROWS) weights_simt_kernel(WeightsParams p
 }  // namespace
 
 // Splits of the keys such that about two blocks land on each SM.
-int tree_simt_splits(int B, int Hq, int Hkv, int Nq, long long capacity) {
+int tree_f32_splits(int B, int Hq, int Hkv, int Nq, long long capacity) {
   const long long blocks = (long long)B * Hkv * (((long long)Nq * (Hq / Hkv) + ROWS - 1) / ROWS);
   const long long tiles = (capacity + Nq + KT - 1) / KT;
   const long long want = std::min((4ll * sm_count() + blocks - 1) / blocks, 65535ll / Hkv);
   return (int)std::max(1ll, std::min(std::min(want, tiles), 64ll));
 }
 
-int launch_tree_simt(const TreeParams& p, cudaStream_t st) {
+int launch_tree_f32(const TreeParams& p, cudaStream_t st) {
   const int G = p.Hq / p.Hkv;
   const dim3 grid((unsigned)(((long long)p.Nq * G + ROWS - 1) / ROWS), (unsigned)(p.Hkv * p.num_splits), (unsigned)p.B);
-  (p.D == 64 ? tree_simt_kernel<float, 64> : tree_simt_kernel<float, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
+  (p.D == 64 ? tree_f32_kernel<64> : tree_f32_kernel<128>)<<<grid, 32 * ROWS, 0, st>>>(p);
   count_launch();
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   return launch_merge(p.o_part, p.lse_part, p.num_splits, p.o, p.lse, p.B, p.Hq, p.Nq, p.D, 1, st);
 }
 
-int launch_weights_simt(const WeightsParams& p, cudaStream_t st) {
+int launch_weights_f32(const WeightsParams& p, cudaStream_t st) {
   const dim3 grid((unsigned)((p.cap + KT - 1) / KT), (unsigned)p.Hkv, (unsigned)p.B);
-  if (p.bf16)
-    (p.D == 64 ? weights_simt_kernel<__nv_bfloat16, 64> : weights_simt_kernel<__nv_bfloat16, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
-  else
-    (p.D == 64 ? weights_simt_kernel<float, 64> : weights_simt_kernel<float, 128>)<<<grid, 32 * ROWS, 0, st>>>(p);
+  (p.D == 64 ? weights_f32_kernel<64> : weights_f32_kernel<128>)<<<grid, 32 * ROWS, 0, st>>>(p);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

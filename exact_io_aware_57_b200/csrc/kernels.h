@@ -160,13 +160,14 @@ int launch_wait_selftest(long long limit_cycles, cudaStream_t st);
 int launch_ex2_selftest(const float* x, float* y, long long n, cudaStream_t st);
 
 // ------------------------------------------------- key/value cache (cache.cuh)
-// Tree attention: row t of sequence b sees its cached slots and the drafted
-// keys j with bit j of its mask row (without a mask: j <= t).
+// A unit of the bf16 tree attention that a cut between CTAs divides:
 // pair2 = 2 * pair + (two row tiles); `more` later parts follow the first one
 // (0: the CTA's run begins no unit that a cut divides).
 struct TreeCut {
   int b, hk, pair2, more;
 };
+// Tree attention: row t of sequence b sees its cached slots and the drafted
+// keys j with bit j of its mask row (without a mask: j <= t).
 struct TreeParams {
   const void *q, *k_new, *v_new;  // k_new / v_new null: no drafted keys
   CacheView c;
@@ -176,7 +177,7 @@ struct TreeParams {
   const int* row_lens;
   void* o;
   float* lse;
-  int B, Hq, Hkv, Nq, D, bf16;
+  int B, Hq, Hkv, Nq, D;
   float scale;
   int num_splits;
   float *o_part, *lse_part;  // fp32 path: as SplitKV's; bf16 path: raw O, and (m, l) pairs
@@ -187,11 +188,15 @@ struct TreeParams {
 };
 size_t tree_sm100_workspace(int Hq, int Hkv, int Nq, int D);
 int launch_tree_sm100(TreeParams p, void* workspace, cudaStream_t st);
-int tree_simt_splits(int B, int Hq, int Hkv, int Nq, long long capacity);
-int launch_tree_simt(const TreeParams& p, cudaStream_t st);
+int tree_f32_splits(int B, int Hq, int Hkv, int Nq, long long capacity);
+int launch_tree_f32(const TreeParams& p, cudaStream_t st);
 
 // out[b, hk, j] = weights[b, hk, j] + sum over counted rows i and the heads of
 // the group of exp(scale q . k_j - lse), j <= len - count + i.
+// A key tile of the bf16 path that a cut between CTAs divides (as TreeCut).
+struct WeightsCut {
+  int b, hk, kt, more;
+};
 struct WeightsParams {
   const void* q;
   const float* lse;
@@ -201,11 +206,16 @@ struct WeightsParams {
   const float* weights;  // null: zeros
   float* out;
   int cap;  // slots per (sequence, KV head) of weights and out
-  int B, Hq, Hkv, Nq, D, bf16;
+  int B, Hq, Hkv, Nq, D;
   float scale;
   int* status;
+  float* part;       // bf16 path: two partial key tiles per CTA
+  WeightsCut* cuts;  // bf16 path: one per CTA
+  long long wait_limit;
 };
-int launch_weights_simt(const WeightsParams& p, cudaStream_t st);
+size_t weights_sm100_workspace();
+int launch_weights_sm100(WeightsParams p, void* workspace, cudaStream_t st);
+int launch_weights_f32(const WeightsParams& p, cudaStream_t st);
 
 struct AppendParams {
   const void *k_new, *v_new;  // rows of row_bytes, n_new per sequence

@@ -68,9 +68,7 @@ struct TreeSmem {
   uint64_t kv_full[NST], kv_empty[NST];
   uint64_t s_full[2], p_full[2];
   uint64_t o_done, o_free, ml_full, drain;
-  long long sum[kThreads / 32];
-  long long start_off;
-  int start_b;
+  RunSmem<kThreads> run;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -198,7 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- setup
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    s.start_b = -1;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.q_full[i], 1);
       mbar_init(&s.q_empty[i], 1);
@@ -222,54 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
 
-  // ---- this CTA's run: all tiles of the batch, then the sequence it starts in
-  long long mine = 0;
-  for (int b = threadIdx.x; b < p.B; b += kThreads) mine += load_seq(p, rw, b).per_head * p.Hkv;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s.sum[warp] = mine;
   tc_fence_before();
-  __syncthreads();
+  const Run run = find_run<kThreads>(s.run, p.B, [&](int b) { return load_seq(p, rw, b).per_head * p.Hkv; });
   tc_fence_after();
-  long long total = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) total += s.sum[i];
-  // as many CTAs as there are tiles at most: each that takes part has a run
-  const long long ctas = min((long long)gridDim.x, total);
-  const long long run0 = min((long long)blockIdx.x, ctas) * total / ctas;
-  const long long run1 = min(blockIdx.x + 1ll, ctas) * total / ctas;
-  long long before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    const long long w = b < p.B ? load_seq(p, rw, b).per_head * p.Hkv : 0;
-    long long x = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s.sum[warp] = x;
-    __syncthreads();
-    long long all = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) x += s.sum[i];
-      all += s.sum[i];
-    }
-    const long long lo = before + x - w;
-    if (lo <= run0 && run0 < lo + w) {
-      s.start_b = b;
-      s.start_off = run0 - lo;
-    }
-    before += all;
-    __syncthreads();
-    if (before > run0) break;  // uniform
-  }
   const uint32_t tmem = s.tmem_base;
   const Abort ab{&s.abort_flag, p.status, p.wait_limit};
   Walk w;
-  w.begin(p, rw, s.start_b, s.start_off, run1 - run0);
+  w.begin(p, rw, run.b, run.off, run.run1 - run.run0);
   Unit u{};
 
   if (warp == kWarpLoad) {
@@ -277,31 +233,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long seq = 0;  // K/V tiles loaded
     int nq = 0;         // Q tiles loaded
     bool ok = true;
-    const int pieces = KT / box_rows;
     auto load_tile = [&](const CUtensorMap* ctx, const CUtensorMap* fresh, const Unit& u, int len, int nc, int tile,
                          long long at) -> bool {
       const int st = (int)(at % NST);
       if (!__all_sync(0xffffffffu, mbar_wait(&s.kv_empty[st], ((at / NST) & 1) ^ 1, ab))) return false;
       uint8_t* dst = s.kv[st];
       if (tile < nc) {
-        const int base = tile * KT;
-        const int live = min(pieces, (len - base + box_rows - 1) / box_rows);
-        if (lane == 0) mbar_expect_tx(&s.kv_full[st], live * box_rows * KB * 128);
-        __syncwarp();
-        const int piece = lane / KB, kb = lane % KB;
-        if (piece < live) {
-          const int slot = base + piece * box_rows;
-          int page = u.b, row = slot;
-          if (p.c.table) {
-            page = __ldg(p.c.table + (long long)u.b * p.c.max_pages + slot / p.c.page_size);
-            row = slot % p.c.page_size;
-            if (page < 0 || page >= p.c.num_pages) {
-              atomicExch(p.status, ATTN_ERR_INVALID);
-              page = p.c.num_pages;  // outside the tensor: zeros are loaded
-            }
-          }
-          tma_load_4d(dst + kb * KT * 128 + piece * box_rows * 128, ctx, &s.kv_full[st], kb * 64, u.hk, row, page);
-        }
+        load_cache_tile<D>(dst, &s.kv_full[st], ctx, p.c, u.b, u.hk, tile * KT, len, box_rows, p.status);
       } else if (lane == 0) {
         mbar_expect_tx(&s.kv_full[st], new_box_rows * KB * 128);
 #pragma unroll
@@ -668,12 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the run's last unit): its later parts are the next CTAs' first ones.
   if (threadIdx.x == 0) {
     TreeCut cut{0, 0, 0, 0};
-    if (run1 > run0 && u.tb == 0 && u.te < u.n) {
-      const long long end = run1 + (u.n - u.te);  // position behind the unit
-      int c = blockIdx.x + 1;
-      while ((c + 1ll) * total / ctas < end) ++c;
-      cut = TreeCut{u.b, u.hk, u.pair * 2 + u.two, c - (int)blockIdx.x};
-    }
+    if (run.run1 > run.run0 && u.tb == 0 && u.te < u.n)
+      cut = TreeCut{u.b, u.hk, u.pair * 2 + u.two, run_parts(run, u.n - u.te)};
     p.cuts[blockIdx.x] = cut;
   }
 }
@@ -741,10 +675,7 @@ int launch_t(TreeParams p, const Rows& rw, cudaStream_t st) {
   const uint64_t qd[4] = {D, Hq, Nq, B}, qs[3] = {D * 2, rq, rq * Nq};
   const uint32_t qb[4] = {64, (uint32_t)rw.gb, (uint32_t)rw.tt, 1};
   const uint64_t kd[4] = {D, Hkv, S, (uint64_t)p.c.num_pages}, ks[3] = {D * 2, rk, rk * S};
-  // boxes that never straddle a page: the largest power of two that divides it
-  int box = KT;
-  if (p.c.table)
-    while (S % box) box >>= 1;
+  const int box = cache_box_rows(p.c);
   const uint32_t kb[4] = {64, 1, (uint32_t)box, 1};
   const int nbox = std::min(KT, (p.Nq + 7) / 8 * 8);
   const uint64_t nd[4] = {D, Hkv, Nq, B}, ns[3] = {D * 2, rk, rk * Nq};

@@ -1,0 +1,541 @@
+// Attention weight received by each cached slot, on sm_100a tensor cores (bf16):
+//   out[b, hk, j] = weights[b, hk, j] + sum_(i, g) exp(scale q_(i, g) . k_j - LSE_(i, g))
+// over the counted rows i that see j and the heads g of the group.
+//
+// The scores are formed transposed, S^T = K Q^T: the 128 keys of a tile are the
+// TMEM lanes and the query rows the columns, so that a thread owns one key, its
+// sum stays in a register, and nothing is reduced across threads.  With the LSE
+// at hand there is no running maximum: each score costs one FMA, one
+// exponential and one addition.  A decode step has few rows and is bound by
+// reading K; a prompt is bound by the exponentials (16 a cycle and SM against
+// 64 scores of 128-wide dot products on the tensor cores).
+//
+// Work.  A unit is one (sequence, KV head, 128-key tile); its steps are the row
+// tiles (up to 128 rows: tt counted rows x gb heads) from the first that sees
+// the tile.  All steps, in unit order, are cut into equal runs, one CTA per SM; a
+// unit that a cut divides leaves partial sums, added in CTA order by
+// weights_finish_kernel.
+//
+//   warps 0..3   sums of the even steps of the run: thread r owns key r
+//   warps 4..7   sums of the odd steps
+//   warp 8       TMEM owner + single-thread tcgen05.mma issuer
+//   warp 9       TMA producer of K tiles, through the page table
+//   warps 10,11  Q rows (by the row list) and their -LSE into shared memory
+//
+// TMEM: four score buffers of 128 columns, step s in buffer s & 3.
+#include <algorithm>
+#include <cstring>
+
+#include "cache.cuh"
+#include "kernels.h"
+
+namespace attn {
+
+namespace {
+
+constexpr int KT = 128;  // keys per tile (TMEM lanes)
+constexpr int BR = 128;  // rows per tile (columns) at most
+constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpQ = 10;
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr int NZ = 8;  // row-term ring
+
+template <int D>
+struct WeightsSmem {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int NK = D == 128 ? 4 : 8, NQ = D == 128 ? 2 : 4;
+  alignas(1024) uint8_t k[NK][kTileBytes];
+  alignas(1024) uint8_t q[NQ][kTileBytes];
+  alignas(16) float z[NZ][BR];  // -LSE log2(e); -inf for a row that counts for nothing
+  alignas(16) int last[NZ][BR];  // last slot the row sees
+  float half[KT];  // the odd steps' sums of a unit
+  uint64_t k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ];
+  uint64_t z_full[NZ], z_empty[NZ], s_full[4], s_empty[4];
+  uint64_t half_full, half_empty, drain;
+  RunSmem<kThreads> run;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Row tiles: tt counted rows x gb heads, gblk blocks of heads.
+struct Rows {
+  int G, gb, tt, gblk;
+};
+
+__host__ __device__ inline Rows row_tiles(int Hq, int Hkv, int max_rows) {
+  Rows r;
+  r.G = Hq / Hkv;
+  r.gb = r.G < BR ? r.G : BR;
+  const int fit = BR / r.gb;
+  r.tt = fit < max_rows ? fit : max_rows;
+  r.gblk = (r.G + r.gb - 1) / r.gb;
+  return r;
+}
+
+// sum over k < n of floor((a k + b) / m), a, b >= 0 (the lattice points below a
+// line, by the Euclidean reduction of a and m).
+ATTN_DEVINL long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long sum = 0;
+  while (n) {
+    sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
+    a %= m;
+    b %= m;
+    const unsigned long long top = (unsigned long long)a * n + b;
+    if (top < m) break;
+    n = (unsigned)(top / m);
+    b = (unsigned)(top % m);
+    const unsigned x = m;
+    m = a;
+    a = x;
+  }
+  return sum;
+}
+
+// One sequence's share: per KV head, key tile kt has its row tiles from
+// first_tile(kt) on, times the blocks of heads.
+struct Seq {
+  int len, cnt, nk, tiles;  // slots, counted rows, key tiles, row tiles (of one block of heads)
+  long long per_head;
+};
+
+ATTN_DEVINL int first_tile(const Rows& rw, const Seq& s, int kt) {
+  const int i = kt * KT - (s.len - s.cnt);  // the first row that sees the tile
+  return i > 0 ? i / rw.tt : 0;
+}
+
+// Steps of the key tiles below kt of a head.
+ATTN_DEVINL long long steps_below(const Rows& rw, const Seq& s, int kt) {
+  const int shift = s.len - s.cnt;
+  const int k0 = shift >= 0 ? shift / KT + 1 : 0;  // the first tile that early rows do not see
+  long long cut = 0;
+  if (kt > k0) cut = floor_sum(kt - k0, rw.tt, KT, k0 * KT - shift);
+  return ((long long)kt * s.tiles - cut) * rw.gblk;
+}
+
+ATTN_DEVINL Seq load_seq(const WeightsParams& p, const Rows& rw, int b) {
+  Seq s;
+  if (!cache_len(p.c, b, p.cap, p.status, s.len) || !row_count(p.row_lens, b, p.max_rows, p.status, s.cnt))
+    s.len = s.cnt = 0;
+  s.nk = s.cnt > 0 ? (s.len + KT - 1) / KT : 0;
+  s.tiles = (s.cnt + rw.tt - 1) / rw.tt;
+  s.per_head = s.nk > 0 ? steps_below(rw, s, s.nk) : 0;
+  return s;
+}
+
+struct Unit {
+  int b, hk, kt;
+  int first;      // first row tile (of a block of heads)
+  int jb, je, n;  // steps [jb, je) of n: row tile first + j / gblk, block of heads j % gblk
+  bool same_q;    // its only row tile is the previous unit's
+};
+
+struct Walk {
+  int b, hk, kt, j;
+  long long left;
+  bool any;
+  Seq s;
+
+  ATTN_DEVINL void begin(const WeightsParams& p, const Rows& rw, const Run& run) {
+    left = run.run1 - run.run0;
+    any = false;
+    if (left <= 0) return;
+    b = run.b;
+    s = load_seq(p, rw, b);
+    hk = (int)(run.off / s.per_head);
+    const long long off = run.off % s.per_head;
+    int lo = 0, hi = s.nk - 1;  // the last tile with steps_below <= off
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (steps_below(rw, s, mid) <= off)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    kt = lo;
+    j = (int)(off - steps_below(rw, s, kt));
+  }
+  ATTN_DEVINL bool next(const WeightsParams& p, const Rows& rw, Unit& u) {
+    if (left <= 0) return false;
+    bool fresh = !any;
+    any = true;
+    if (kt == s.nk) {
+      kt = 0;
+      fresh = true;
+      if (++hk == p.Hkv) {
+        hk = 0;
+        do s = load_seq(p, rw, ++b);
+        while (s.per_head == 0);
+      }
+    }
+    u.b = b;
+    u.hk = hk;
+    u.kt = kt;
+    u.first = first_tile(rw, s, kt);
+    u.n = (s.tiles - u.first) * rw.gblk;
+    u.jb = j;
+    u.je = (int)min((long long)u.n, j + left);
+    u.same_q = !fresh && s.tiles * rw.gblk == 1;
+    left -= u.je - u.jb;
+    j = 0;
+    ++kt;
+    return true;
+  }
+};
+
+template <int N>
+ATTN_DEVINL void reg_fence(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Sum of exponentials of N columns of a key: x = s * sc2 + z.
+template <int N>
+ATTN_DEVINL void add_columns(const uint32_t (&sr)[N], const float* z, const int* last, bool edge, int key, float sc2,
+                             float& a0, float& a1) {
+#pragma unroll
+  for (int e = 0; e < N; e += 4) {
+    const float4 zz = *reinterpret_cast<const float4*>(z + e);
+    float x0 = fmaf(__uint_as_float(sr[e]), sc2, zz.x), x1 = fmaf(__uint_as_float(sr[e + 1]), sc2, zz.y);
+    float x2 = fmaf(__uint_as_float(sr[e + 2]), sc2, zz.z), x3 = fmaf(__uint_as_float(sr[e + 3]), sc2, zz.w);
+    if (edge) {
+      const int4 ll = *reinterpret_cast<const int4*>(last + e);
+      if (key > ll.x) x0 = -INFINITY;
+      if (key > ll.y) x1 = -INFINITY;
+      if (key > ll.z) x2 = -INFINITY;
+      if (key > ll.w) x3 = -INFINITY;
+    }
+    a0 += ex2(x0) + ex2(x2);
+    a1 += ex2(x1) + ex2(x3);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    weights_kernel(const __grid_constant__ CUtensorMap tm_k, const WeightsParams p, const int box_rows) {
+  using Smem = WeightsSmem<D>;
+  constexpr int NK = Smem::NK, NQ = Smem::NQ;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Rows rw = row_tiles(p.Hq, p.Hkv, p.max_rows);
+  if (threadIdx.x == 0) {
+    s.abort_flag = 0;
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.k_empty[i], 1);
+    }
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(&s.q_full[i], 2);  // the two loading warps
+      mbar_init(&s.q_empty[i], 1);
+    }
+    for (int i = 0; i < NZ; ++i) {
+      mbar_init(&s.z_full[i], 2);
+      mbar_init(&s.z_empty[i], 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.s_empty[i], 4);
+    }
+    mbar_init(&s.half_full, 4);
+    mbar_init(&s.half_empty, 4);
+    mbar_init(&s.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(&s.tmem_base, kTmemCols);
+  if (warp == kWarpLoad && lane == 0) tma_prefetch_desc(&tm_k);
+  tc_fence_before();
+  const Run run = find_run<kThreads>(s.run, p.B, [&](int b) { return load_seq(p, rw, b).per_head * p.Hkv; });
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  const Abort ab{&s.abort_flag, p.status, p.wait_limit};
+  Walk w;
+  w.begin(p, rw, run);
+  Unit u{};
+
+  if (warp == kWarpLoad) {
+    // ===================================================== K producer
+    int i = 0;
+    bool ok = true;
+    for (; ok && w.next(p, rw, u); ++i) {
+      const int st = i % NK;
+      ok = __all_sync(0xffffffffu, mbar_wait(&s.k_empty[st], ((i / NK) & 1) ^ 1, ab));
+      if (ok)
+        load_cache_tile<D>(s.k[st], &s.k_full[st], &tm_k, p.c, u.b, u.hk, u.kt * KT, w.s.len, box_rows, p.status);
+    }
+    if (s.abort_flag) {
+      // leave no copy in flight into shared memory that is about to be released
+      for (int st = 0; st < NK; ++st) {
+        mbar_wait_drain(&s.k_full[st], 0, p.wait_limit / 64);
+        mbar_wait_drain(&s.k_full[st], 1, p.wait_limit / 64);
+      }
+    }
+  } else if (warp >= kWarpQ) {
+    // ===================================================== Q rows
+    // Warp y loads rows [64 y, 64 y + 64) of each row tile: addresses a row per
+    // lane, then 16 bytes per lane and copy, in the 128-byte swizzle (chunk c of
+    // row r at chunk c ^ (r & 7)) that the products read.
+    constexpr int CH = D / 8;  // 16-byte chunks per row
+    const int half = warp - kWarpQ;
+    int i = 0;  // row tiles loaded
+    bool ok = true;
+    while (ok && w.next(p, rw, u)) {
+      if (u.same_q) continue;
+      for (int j = u.jb; ok && j < u.je; ++j, ++i) {
+        const int st = i % NQ, zt = i % NZ;
+        const int i0 = (u.first + j / rw.gblk) * rw.tt, g0 = j % rw.gblk * rw.gb;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.z_empty[zt], ((i / NZ) & 1) ^ 1, ab) &&
+                                         mbar_wait(&s.q_empty[st], ((i / NQ) & 1) ^ 1, ab));
+        if (!ok) break;
+        const uint32_t qs = smem_u32(s.q[st]);
+#pragma unroll 1
+        for (int blk = 0; blk < 2; ++blk) {
+          const int r = half * 64 + blk * 32 + lane, row = i0 + r / rw.gb, g = g0 + r % rw.gb;
+          long long src = -1;
+          float z = -INFINITY;
+          int last = -1;
+          if (r < rw.gb * rw.tt && row < w.s.cnt && g < rw.G) {
+            const int t = p.rows ? __ldg(p.rows + (long long)u.b * p.max_rows + row) : row;
+            if (t < 0 || t >= p.Nq) {
+              atomicExch(p.status, ATTN_ERR_INVALID);
+            } else {
+              const int h = u.hk * rw.G + g;
+              src = (((long long)u.b * p.Nq + t) * p.Hq + h) * D;
+              const float lse = __ldg(p.lse + ((long long)u.b * p.Hq + h) * p.Nq + t);
+              z = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+              last = w.s.len - w.s.cnt + row;
+            }
+          }
+          s.z[zt][r] = z;
+          s.last[zt][r] = last;
+          const char* base = static_cast<const char*>(p.q);
+#pragma unroll 4
+          for (int x = 0; x < CH; ++x) {
+            const int rr = x * (32 / CH) + lane / CH, c = lane % CH;  // row of the block, chunk of the row
+            const long long at = __shfl_sync(0xffffffffu, src, rr);
+            const int r2 = half * 64 + blk * 32 + rr;
+            const uint32_t dst = qs + (c >> 3) * (BR * 128) + r2 * 128 + (((c & 7) ^ (r2 & 7)) << 4);
+            // a row that counts for nothing is zeros
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                         "l"(base + (at < 0 ? 0 : at * 2 + c * 16)), "r"(at < 0 ? 0 : 16)
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s.q_full[st]);
+          mbar_arrive(&s.z_full[zt]);
+        }
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ===================================================== MMA issuer
+    if (lane == 0) {
+      const int width = min(BR, (rw.gb * rw.tt + 15) / 16 * 16);
+      const uint32_t idesc = idesc_bf16(KT, width, 0, 0);
+      int i = 0, iq = -1, step = 0;
+      bool ok = true;
+      for (; ok && w.next(p, rw, u); ++i) {
+        const int kst = i % NK;
+        if (!(ok = mbar_wait(&s.k_full[kst], (i / NK) & 1, ab))) break;
+        for (int j = u.jb; j < u.je; ++j, ++step) {
+          if (!u.same_q) {
+            if (iq >= 0) mma_commit(&s.q_empty[iq % NQ]);  // the previous row tile has been used
+            ++iq;
+            if (!(ok = mbar_wait(&s.q_full[iq % NQ], (iq / NQ) & 1, ab))) break;
+          }
+          const int buf = step & 3;
+          if (!(ok = mbar_wait(&s.s_empty[buf], ((step >> 2) & 1) ^ 1, ab))) break;
+          tc_fence_after();
+          const uint32_t ka = smem_u32(s.k[kst]), qa = smem_u32(s.q[iq % NQ]);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + buf * BR, sdesc_sw128(ka + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024),
+                   sdesc_sw128(qa + (kk >> 2) * (BR * 128) + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
+          mma_commit(&s.s_full[buf]);
+        }
+        if (ok) mma_commit(&s.k_empty[kst]);
+      }
+      // TMEM must be quiescent before it is released
+      mma_commit(&s.drain);
+      mbar_wait_drain(&s.drain, 0, p.wait_limit);
+    }
+  } else {
+    // ===================================================== sums
+    const int wg = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const float sc2 = p.scale * kLog2e;
+    const int width = min(BR, (rw.gb * rw.tt + 15) / 16 * 16);
+    int step = 0, iz = -1, shared = 0;
+    bool ok = true;
+    while (ok && w.next(p, rw, u)) {
+      const int key = u.kt * KT + r, n = u.je - u.jb;
+      const bool whole = n == u.n;
+      // whose sum is final: of one step its warpgroup's, else the first's
+      const bool owner = n == 1 ? (step & 1) == wg : wg == 0;
+      const long long at = ((long long)u.b * p.Hkv + u.hk) * p.cap + key;
+      float before = 0.f;
+      if (owner && whole && key < w.s.len && p.weights) before = p.weights[at];
+      float sum = 0.f;
+      for (int j = u.jb; j < u.je; ++j, ++step) {
+        if (!u.same_q) {
+          if (iz >= 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.z_empty[iz % NZ]);
+          }
+          ++iz;
+          ok = __all_sync(0xffffffffu, mbar_wait(&s.z_full[iz % NZ], (iz / NZ) & 1, ab));
+          if (!ok) break;
+        }
+        if ((step & 1) != wg) continue;
+        const int buf = step & 3;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (step >> 2) & 1, ab));
+        if (!ok) break;
+        tc_fence_after();
+        const float* z = s.z[iz % NZ];
+        const int* last = s.last[iz % NZ];
+        const uint32_t col = tmem + lane_off + buf * BR;
+        // rows from i0 on; the tile's last key is hidden from the first of them
+        const int i0 = (u.first + j / rw.gblk) * rw.tt;
+        const bool edge = u.kt * KT + KT - 1 > w.s.len - w.s.cnt + i0;
+        float a0 = 0.f, a1 = 0.f;  // a tile's own sums: short chains round less
+        int c = 0;
+        for (; c + 32 <= width; c += 32) {
+          uint32_t sr[32];
+          tmem_ld32(col + c, sr);
+          tmem_wait_ld();
+          reg_fence(sr);
+          add_columns(sr, z + c, last + c, edge, key, sc2, a0, a1);
+        }
+        if (c < width) {
+          uint32_t sr[16];
+          tmem_ld16(col + c, sr);
+          tmem_wait_ld();
+          reg_fence(sr);
+          add_columns(sr, z + c, last + c, edge, key, sc2, a0, a1);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.s_empty[buf]);
+        sum += a0 + a1;
+      }
+      if (!ok) break;
+      if (n > 1) {  // both warpgroups took steps
+        if (wg == 1) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&s.half_empty, (shared & 1) ^ 1, ab));
+          if (!ok) break;
+          s.half[r] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.half_full);
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(&s.half_full, shared & 1, ab));
+          if (!ok) break;
+          sum += s.half[r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.half_empty);
+        }
+        ++shared;
+      }
+      if (owner) {
+        if (!whole)
+          p.part[((long long)blockIdx.x * 2 + (u.jb > 0 ? 0 : 1)) * KT + r] = sum;
+        else if (key < w.s.len)
+          p.out[at] = before + sum;
+      }
+    }
+  }
+
+  // ---- teardown; the finishing kernel may be launched (it waits for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  // The unit that this run ends in the middle of, having held its beginning (u is
+  // the run's last unit): its later parts are the next CTAs' first ones.
+  if (threadIdx.x == 0) {
+    WeightsCut cut{0, 0, 0, 0};
+    if (run.run1 > run.run0 && u.jb == 0 && u.je < u.n)
+      cut = WeightsCut{u.b, u.hk, u.kt, run_parts(run, u.n - u.je)};
+    p.cuts[blockIdx.x] = cut;
+  }
+}
+
+// The first blocks add the parts of the units that a cut divides, in CTA order;
+// when out is another buffer than weights, all blocks copy the slots that no
+// unit covers (behind each sequence's end).
+__global__ void __launch_bounds__(KT) weights_finish_kernel(const WeightsParams p, const int ctas) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int r = threadIdx.x;
+  if ((int)blockIdx.x < ctas) {
+    const WeightsCut cut = p.cuts[blockIdx.x];
+    const int key = cut.kt * KT + r;
+    if (cut.more > 0 && key < p.c.lens[cut.b]) {
+      float sum = p.part[((long long)blockIdx.x * 2 + 1) * KT + r];
+      for (int i = 1; i <= cut.more; ++i) sum += p.part[(long long)(blockIdx.x + i) * 2 * KT + r];
+      const long long at = ((long long)cut.b * p.Hkv + cut.hk) * p.cap + key;
+      p.out[at] = (p.weights ? p.weights[at] : 0.f) + sum;
+    }
+  }
+  if (p.weights == p.out) return;
+  for (long long u = blockIdx.x; u < (long long)p.B * p.Hkv; u += gridDim.x) {
+    int len, cnt;
+    const int b = (int)(u / p.Hkv);
+    // a sequence that is not acceptable is left as it is
+    if (!cache_len(p.c, b, p.cap, p.status, len) || !row_count(p.row_lens, b, p.max_rows, p.status, cnt)) continue;
+    for (int j = (cnt > 0 ? len : 0) + r; j < p.cap; j += KT)
+      p.out[u * p.cap + j] = p.weights ? p.weights[u * p.cap + j] : 0.f;
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <int D>
+int launch_t(const WeightsParams& p, cudaStream_t st) {
+  CUtensorMap mk;
+  const uint64_t row = (uint64_t)p.Hkv * D * 2;
+  const uint64_t kd[4] = {D, (uint64_t)p.Hkv, (uint64_t)p.c.page_size, (uint64_t)p.c.num_pages};
+  const uint64_t ks[3] = {D * 2, row, row * p.c.page_size};
+  const int box = cache_box_rows(p.c);
+  const uint32_t kb[4] = {64, 1, (uint32_t)box, 1};
+  int rc;
+  if ((rc = encode_tmap_bf16(&mk, p.c.k, 4, kd, ks, kb))) return rc;
+  const size_t smem = sizeof(WeightsSmem<D>) + 1024;
+  static_assert(sizeof(WeightsSmem<D>) + 1024 <= 232448, "shared memory");
+  if (cudaFuncSetAttribute(weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  const int ctas = sm_count();
+  weights_kernel<D><<<ctas, kThreads, smem, st>>>(mk, p, box);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::max<long long>(ctas, std::min<long long>((long long)p.B * p.Hkv, 4ll * ctas)));
+  cfg.blockDim = dim3(KT);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, weights_finish_kernel, p, ctas) != cudaSuccess) return ATTN_ERR_CUDA;
+  count_launch(2);
+  return ATTN_OK;
+}
+
+}  // namespace
+
+size_t weights_sm100_workspace() {
+  return align256((size_t)sm_count() * 2 * KT * 4) + align256((size_t)sm_count() * sizeof(WeightsCut));
+}
+
+int launch_weights_sm100(WeightsParams p, void* workspace, cudaStream_t st) {
+  p.part = static_cast<float*>(workspace);
+  p.cuts = reinterpret_cast<WeightsCut*>(static_cast<char*>(workspace) + align256((size_t)sm_count() * 2 * KT * 4));
+  p.wait_limit = kWaitLimitCycles;
+  return p.D == 64 ? launch_t<64>(p, st) : launch_t<128>(p, st);
+}
+
+}  // namespace attn
