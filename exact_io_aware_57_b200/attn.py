@@ -9,6 +9,7 @@ missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from pathlib import Path
@@ -402,38 +403,72 @@ class KVCache(ctypes.Structure):
                 ("max_pages", _I)]
 
 
-def _like(t, name, dtype, shape, device):
-    """t as a device pointer once its dtype, shape (None: any extent) and device are as stated."""
-    if t.dtype != dtype:
-        raise AttnError(f"{name} must be {dtype}")
-    if len(t.shape) != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
+# A decode step makes several of these calls per layer, each of a few
+# microseconds on the device, so their checks are few and cheap: one test per
+# tensor, and the reasons only where it fails.
+def _ptr(t, name, dtype, shape, dev):
+    """Device address of t, a contiguous tensor of this dtype, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise AttnError(f"{name} must be {dtype}, is {t.dtype}")
+    if t.shape != shape:
         raise AttnError(f"{name} must have shape {list(shape)}, has {list(t.shape)}")
-    if t.device != device:
-        raise AttnError(f"{name} is on {t.device}, not on {device}")
-    return _dev(t, name)
+    if t.device != dev:
+        raise AttnError(f"{name} is on {t.device}, not on {dev}")
+    raise AttnError(f"{name} must be contiguous")
 
 
-def _cache(k, v, lens, block_table, B, Hkv, d, dtype, device, name="cache"):
-    c = KVCache()
-    c.k = _like(k, f"k_{name}", dtype, (None, None, Hkv, d), device)
-    c.v = None if v is None else _like(v, f"v_{name}", dtype, tuple(k.shape), device)
-    c.num_pages, c.page_size = k.shape[0], k.shape[1]
-    c.lens = None if lens is None else _like(lens, "cache_lens", torch.int32, (B,), device)
-    if block_table is not None:
-        c.block_table = _like(block_table, "block_table", torch.int32, (B, None), device)
-        c.max_pages = block_table.shape[1]
-    return c
+def _cache(k, v, lens, table, B, Hkv, d, dtype, dev, name="cache"):
+    shape = k.shape
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != d:
+        raise AttnError(f"k_{name} must be [pages, page_size, {Hkv}, {d}], has {list(shape)}")
+    tp, width = None, 1
+    if table is not None:
+        width = table.shape[-1]
+        tp = _ptr(table, "block_table", torch.int32, (B, width), dev)
+    return KVCache(_ptr(k, f"k_{name}", dtype, shape, dev), None if v is None else _ptr(v, f"v_{name}", dtype, shape, dev),
+                   tp, None if lens is None else _ptr(lens, "cache_lens", torch.int32, (B,), dev), shape[0], shape[1],
+                   width)
 
 
-def _rows_args(rows, row_lens, B, n, device):
-    """Pointers and width of the optional row list and row counts."""
-    rp = None if rows is None else _like(rows, "rows", torch.int32, (B, None), device)
-    lp = None if row_lens is None else _like(row_lens, "row_lens", torch.int32, (B,), device)
-    return rp, n if rows is None else rows.shape[1], lp
+def _row_args(rows, row_lens, B, n, dev):
+    """Addresses and width of the optional row list and row counts."""
+    rp, width = None, n
+    if rows is not None:
+        width = rows.shape[-1]
+        rp = _ptr(rows, "rows", torch.int32, (B, width), dev)
+    return rp, width, None if row_lens is None else _ptr(row_lens, "row_lens", torch.int32, (B,), dev)
 
 
-def _cache_stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _on(t, name):
+    """t's device, and a context in which it is the current one."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise AttnError(f"{name} must be a CUDA tensor")
+    return dev, _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise AttnError(f"{name} must have {n} dimensions, has {list(t.shape)}")
+    return t.shape
+
+
+def _stream_on(stream, dev) -> int:
+    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+
+def _scratch(workspace, size, dev):
+    """Address and bytes of the caller's workspace, or of a new one (returned to keep it alive)."""
+    if workspace is None:
+        workspace = torch.empty(size, device=dev, dtype=torch.uint8)
+    elif workspace.device != dev:
+        raise AttnError(f"workspace is on {workspace.device}, not on {dev}")
+    return workspace, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
 
 
 def attn_cache_append(k_new, v_new, k_cache, v_cache, cache_lens, block_table=None, rows=None, row_lens=None,
@@ -443,22 +478,24 @@ def attn_cache_append(k_new, v_new, k_cache, v_cache, cache_lens, block_table=No
     int32 [B, max_pages]; without a table page b is sequence b's): slot cache_lens[b] + i
     takes row rows[b, i] (default i), i < row_lens[b] (default all).  Returns the new
     lengths, int32 [B], in a buffer of their own; cache_lens is not changed."""
-    B, T, Hkv, d = k_new.shape
-    dev = k_new.device
-    c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, k_new.dtype, dev)
-    rp, width, lp = _rows_args(rows, row_lens, B, T, dev)
-    new_lens = torch.empty_like(cache_lens) if new_lens is None else new_lens
-    with torch.cuda.device(dev):
-        _check(_lib.attn_cache_append(_dev(k_new, "k_new"), _like(v_new, "v_new", k_new.dtype, k_new.shape, dev),
+    B, T, Hkv, d = shape = _dims(k_new, "k_new", 4)
+    dt = k_new.dtype
+    dev, here = _on(k_new, "k_new")
+    with here:
+        c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, dt, dev)
+        rp, width, lp = _row_args(rows, row_lens, B, T, dev)
+        if new_lens is None:
+            new_lens = torch.empty_like(cache_lens)
+        _check(_lib.attn_cache_append(_ptr(k_new, "k_new", dt, shape, dev), _ptr(v_new, "v_new", dt, shape, dev),
                                       ctypes.byref(c), rp, width, lp,
-                                      _like(new_lens, "new_lens", torch.int32, (B,), dev), B, T, Hkv, d,
-                                      _dtype_code(k_new), _cache_stream(stream, dev)))
+                                      _ptr(new_lens, "new_lens", torch.int32, (B,), dev), B, T, Hkv, d,
+                                      _dtype_code(k_new), _stream_on(stream, dev)))
     return new_lens
 
 
 def attn_fwd_tree_workspace_size(batch, h_q, h_kv, n_q, d, dtype=torch.bfloat16) -> int:
-    return int(_lib.attn_fwd_tree_workspace_size(batch, h_q, h_kv, n_q, d, ATTN_F32 if dtype == torch.float32 else
-                                                 ATTN_BF16))
+    return int(_lib.attn_fwd_tree_workspace_size(batch, h_q, h_kv, n_q, d,
+                                                 ATTN_F32 if dtype == torch.float32 else ATTN_BF16))
 
 
 def attn_fwd_tree(q, k_cache, v_cache, cache_lens, k_new=None, v_new=None, block_table=None, tree_mask=None,
@@ -468,39 +505,41 @@ def attn_fwd_tree(q, k_cache, v_cache, cache_lens, k_new=None, v_new=None, block
     j % 64 of tree_mask[(b,) t, j // 64] set (int64 [B,T,ceil(T/64)] or [T,ceil(T/64)];
     default j <= t).  Without k_new the rows see the cache only.  Rows t >= row_lens[b] and
     rows that see no key get O = 0, LSE = -inf.  T = 1 is a decode step."""
-    B, T, Hq, d = q.shape
-    Hkv = k_cache.shape[2]
-    dev = q.device
+    B, T, Hq, d = shape = _dims(q, "q", 4)
+    Hkv, dt = _dims(k_cache, "k_cache", 4)[2], q.dtype
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, q.dtype, dev)
     if (k_new is None) != (v_new is None):
         raise AttnError("pass k_new and v_new together")
-    kp = None if k_new is None else _like(k_new, "k_new", q.dtype, (B, T, Hkv, d), dev)
-    vp = None if v_new is None else _like(v_new, "v_new", q.dtype, (B, T, Hkv, d), dev)
-    mp, mstride = None, 0
-    if tree_mask is not None:
-        words = (T + 63) // 64
-        per = tree_mask.dim() == 3
-        mp = _like(tree_mask, "tree_mask", torch.int64, (B, T, words) if per else (T, words), dev)
-        mstride = T * words if per else 0
-    _, _, lp = _rows_args(None, row_lens, B, T, dev)
-    o = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, T), device=dev, dtype=torch.float32) if lse is None else lse
-    if workspace is None:
-        workspace = torch.empty(attn_fwd_tree_workspace_size(B, Hq, Hkv, T, d, q.dtype), device=dev,
-                                dtype=torch.uint8)
-    with torch.cuda.device(dev):
-        _check(_lib.attn_fwd_tree(_dev(q, "q"), kp, vp, ctypes.byref(c), mp, mstride, lp,
-                                  _like(o, "out", q.dtype, q.shape, dev),
-                                  _like(lse, "lse", torch.float32, (B, Hq, T), dev), B, Hq, Hkv, T, d, scale,
-                                  _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                                  _dtype_code(q), _cache_stream(stream, dev)))
+    if tree_mask is not None and k_new is None:
+        raise AttnError("tree_mask needs k_new and v_new")
+    dev, here = _on(q, "q")
+    with here:
+        c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, dt, dev)
+        new = (B, T, Hkv, d)
+        kp = None if k_new is None else _ptr(k_new, "k_new", dt, new, dev)
+        vp = None if v_new is None else _ptr(v_new, "v_new", dt, new, dev)
+        mp, mstride = None, 0
+        if tree_mask is not None:
+            words = (T + 63) // 64
+            if tree_mask.dim() == 3:
+                mp, mstride = _ptr(tree_mask, "tree_mask", torch.int64, (B, T, words), dev), T * words
+            else:
+                mp = _ptr(tree_mask, "tree_mask", torch.int64, (T, words), dev)
+        lp = None if row_lens is None else _ptr(row_lens, "row_lens", torch.int32, (B,), dev)
+        o = torch.empty_like(q) if out is None else out
+        if lse is None:
+            lse = torch.empty((B, Hq, T), device=dev, dtype=torch.float32)
+        size = 0 if workspace is not None else attn_fwd_tree_workspace_size(B, Hq, Hkv, T, d, dt)
+        workspace, wp, wbytes = _scratch(workspace, size, dev)
+        _check(_lib.attn_fwd_tree(_ptr(q, "q", dt, shape, dev), kp, vp, ctypes.byref(c), mp, mstride, lp,
+                                  _ptr(o, "out", dt, shape, dev), _ptr(lse, "lse", torch.float32, (B, Hq, T), dev), B,
+                                  Hq, Hkv, T, d, scale, wp, wbytes, _dtype_code(q), _stream_on(stream, dev)))
     return o, lse
 
 
 def attn_cache_weights_workspace_size(batch, h_q, h_kv, d, dtype=torch.bfloat16) -> int:
-    return int(_lib.attn_cache_weights_workspace_size(batch, h_q, h_kv, d, ATTN_F32 if dtype == torch.float32 else
-                                                      ATTN_BF16))
+    return int(_lib.attn_cache_weights_workspace_size(batch, h_q, h_kv, d,
+                                                      ATTN_F32 if dtype == torch.float32 else ATTN_BF16))
 
 
 def attn_cache_weights(q, lse, k_cache, cache_lens, weights, block_table=None, rows=None, row_lens=None, scale=None,
@@ -510,25 +549,25 @@ def attn_cache_weights(q, lse, k_cache, cache_lens, weights, block_table=None, r
     all), of q [B,T,Hq,d] with their lse [B,Hq,T], each summed over the query heads of a
     group; row i sees the slots j <= cache_lens[b] - count + i.  weights None: zeros, of
     one page's or the table's capacity.  out: the result (default weights itself)."""
-    B, T, Hq, d = q.shape
-    Hkv = k_cache.shape[2]
-    dev = q.device
+    B, T, Hq, d = shape = _dims(q, "q", 4)
+    Hkv, dt = _dims(k_cache, "k_cache", 4)[2], q.dtype
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    c = _cache(k_cache, None, cache_lens, block_table, B, Hkv, d, q.dtype, dev)
-    rp, width, lp = _rows_args(rows, row_lens, B, T, dev)
-    if out is None:
-        cap = c.page_size * (c.max_pages if block_table is not None else 1)
-        out = torch.empty((B, Hkv, cap), device=dev, dtype=torch.float32) if weights is None else weights
-    op = _like(out, "out", torch.float32, (B, Hkv, None), dev)
-    wp = None if weights is None else _like(weights, "weights", torch.float32, tuple(out.shape), dev)
-    if workspace is None:
-        workspace = torch.empty(attn_cache_weights_workspace_size(B, Hq, Hkv, d, q.dtype), device=dev,
-                                dtype=torch.uint8)
-    with torch.cuda.device(dev):
-        _check(_lib.attn_cache_weights(_dev(q, "q"), _like(lse, "lse", torch.float32, (B, Hq, T), dev),
-                                       ctypes.byref(c), rp, width, lp, wp, op, out.shape[2], B, Hq, Hkv, T, d, scale,
-                                       _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                                       _dtype_code(q), _cache_stream(stream, dev)))
+    dev, here = _on(q, "q")
+    with here:
+        c = _cache(k_cache, None, cache_lens, block_table, B, Hkv, d, dt, dev)
+        rp, width, lp = _row_args(rows, row_lens, B, T, dev)
+        if out is None:
+            out = weights
+            if out is None:
+                out = torch.empty((B, Hkv, c.page_size * c.max_pages), device=dev, dtype=torch.float32)
+        cap = out.shape[-1]
+        op = _ptr(out, "out", torch.float32, (B, Hkv, cap), dev)
+        wp = None if weights is None else _ptr(weights, "weights", torch.float32, (B, Hkv, cap), dev)
+        size = 0 if workspace is not None else attn_cache_weights_workspace_size(B, Hq, Hkv, d, dt)
+        workspace, sp, sbytes = _scratch(workspace, size, dev)
+        _check(_lib.attn_cache_weights(_ptr(q, "q", dt, shape, dev), _ptr(lse, "lse", torch.float32, (B, Hq, T), dev),
+                                       ctypes.byref(c), rp, width, lp, wp, op, cap, B, Hq, Hkv, T, d, scale, sp, sbytes,
+                                       _dtype_code(q), _stream_on(stream, dev)))
     return out
 
 
@@ -539,21 +578,28 @@ def attn_cache_evict(k_cache, v_cache, weights, cache_lens, keep, k_out, v_out, 
     ascending order to the cache k_out / v_out (out_table), whose pages are others than the
     source's.  Returns weights_out (like weights, zeros behind the last slot), kept int32
     [B,Hkv,keep] (source slots, -1 behind the last) and new_lens int32 [B]."""
-    Hkv, d = k_cache.shape[2], k_cache.shape[3]
-    B, dev = weights.shape[0], k_cache.device
+    _, _, Hkv, d = _dims(k_cache, "k_cache", 4)
+    B, _, cap = wshape = _dims(weights, "weights", 3)
+    dt = k_cache.dtype
     keep, recent = int(keep), int(recent)
-    src = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, k_cache.dtype, dev)
-    dst = _cache(k_out, v_out, None, out_table, B, Hkv, d, k_cache.dtype, dev, name="out")
-    wp = _like(weights, "weights", torch.float32, (B, Hkv, None), dev)
-    weights_out = torch.empty_like(weights) if weights_out is None else weights_out
-    kept = torch.empty((B, Hkv, max(keep, 0)), device=dev, dtype=torch.int32) if kept is None else kept
-    new_lens = torch.empty_like(cache_lens) if new_lens is None else new_lens
-    with torch.cuda.device(dev):
-        _check(_lib.attn_cache_evict(ctypes.byref(src), wp, weights.shape[2], keep, recent, ctypes.byref(dst),
-                                     _like(weights_out, "weights_out", torch.float32, tuple(weights.shape), dev),
-                                     _like(kept, "kept", torch.int32, (B, Hkv, keep), dev),
-                                     _like(new_lens, "new_lens", torch.int32, (B,), dev), B, Hkv, d,
-                                     _dtype_code(k_cache), _cache_stream(stream, dev)))
+    if not 0 <= recent <= keep or keep == 0:
+        raise AttnError("need 0 <= recent <= keep and keep > 0")
+    dev, here = _on(k_cache, "k_cache")
+    with here:
+        src = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, dt, dev)
+        dst = _cache(k_out, v_out, None, out_table, B, Hkv, d, dt, dev, name="out")
+        wp = _ptr(weights, "weights", torch.float32, (B, Hkv, cap), dev)
+        if weights_out is None:
+            weights_out = torch.empty_like(weights)
+        if kept is None:
+            kept = torch.empty((B, Hkv, keep), device=dev, dtype=torch.int32)
+        if new_lens is None:
+            new_lens = torch.empty_like(cache_lens)
+        _check(_lib.attn_cache_evict(ctypes.byref(src), wp, cap, keep, recent, ctypes.byref(dst),
+                                     _ptr(weights_out, "weights_out", torch.float32, wshape, dev),
+                                     _ptr(kept, "kept", torch.int32, (B, Hkv, keep), dev),
+                                     _ptr(new_lens, "new_lens", torch.int32, (B,), dev), B, Hkv, d,
+                                     _dtype_code(k_cache), _stream_on(stream, dev)))
     return weights_out, kept, new_lens
 
 

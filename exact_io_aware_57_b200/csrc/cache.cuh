@@ -135,31 +135,45 @@ ATTN_DEVINL int run_parts(const Run& r, long long rest) {
   return c - (int)blockIdx.x;
 }
 
-// Load the 128-key tile that begins at slot `base` (below len) of sequence b and
-// KV head hk into dst (64-element blocks of 128 rows each), all lanes of a warp
-// taking part: boxes of box_rows slots that never straddle a page, a lane per
-// box.  Rows behind the last box that begins below len are not written.
+// Where a lane's box of a 128-key tile of cached slots lies: boxes of box_rows
+// slots that never straddle a page, lane = (piece of the tile, 64-element block).
+// Looked up a tile ahead of its load, so that no load waits for the page table.
+struct TileBox {
+  int page, row, live;  // live: boxes of the tile that begin below the length
+};
+
 template <int D>
-ATTN_DEVINL void load_cache_tile(uint8_t* dst, uint64_t* bar, const CUtensorMap* map, const CacheView& c, int b, int hk,
-                                 int base, int len, int box_rows, int* status) {
+ATTN_DEVINL TileBox find_box(const CacheView& c, int b, int base, int len, int box_rows) {
+  const int lane = threadIdx.x & 31;
+  TileBox t;
+  t.live = min(128 / box_rows, (len - base + box_rows - 1) / box_rows);
+  const int piece = lane / (D / 64), slot = base + piece * box_rows;
+  t.page = b;
+  t.row = slot;
+  if (c.table && piece < t.live) {
+    t.page = __ldg(c.table + (long long)b * c.max_pages + slot / c.page_size);
+    t.row = slot % c.page_size;
+  }
+  return t;
+}
+
+// Load that tile of KV head hk into dst (64-element blocks of 128 rows each), all
+// lanes of a warp taking part.  Rows behind its last live box are not written.
+template <int D>
+ATTN_DEVINL void load_cache_tile(uint8_t* dst, uint64_t* bar, const CUtensorMap* map, const CacheView& c,
+                                 const TileBox& t, int hk, int box_rows, int* status) {
   constexpr int KB = D / 64;
   const int lane = threadIdx.x & 31;
-  const int live = min(128 / box_rows, (len - base + box_rows - 1) / box_rows);
-  if (lane == 0) mbar_expect_tx(bar, live * box_rows * KB * 128);
+  if (lane == 0) mbar_expect_tx(bar, t.live * box_rows * KB * 128);
   __syncwarp();
   const int piece = lane / KB, kb = lane % KB;
-  if (piece < live) {
-    const int slot = base + piece * box_rows;
-    int page = b, row = slot;
-    if (c.table) {
-      page = __ldg(c.table + (long long)b * c.max_pages + slot / c.page_size);
-      row = slot % c.page_size;
-      if (page < 0 || page >= c.num_pages) {
-        atomicExch(status, ATTN_ERR_INVALID);
-        page = c.num_pages;  // outside the tensor: zeros are loaded
-      }
+  if (piece < t.live) {
+    int page = t.page;
+    if (page < 0 || page >= c.num_pages) {
+      atomicExch(status, ATTN_ERR_INVALID);
+      page = c.num_pages;  // outside the tensor: zeros are loaded
     }
-    tma_load_4d(dst + kb * 128 * 128 + piece * box_rows * 128, map, bar, kb * 64, hk, row, page);
+    tma_load_4d(dst + kb * 128 * 128 + piece * box_rows * 128, map, bar, kb * 64, hk, t.row, page);
   }
   __syncwarp();
 }

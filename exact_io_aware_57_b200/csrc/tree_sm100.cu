@@ -230,53 +230,76 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpLoad) {
     // ===================================================== TMA producer
-    long long seq = 0;  // K/V tiles loaded
+    uint32_t seq = 0;  // K/V tiles loaded
     int nq = 0;         // Q tiles loaded
     bool ok = true;
-    auto load_tile = [&](const CUtensorMap* ctx, const CUtensorMap* fresh, const Unit& u, int len, int nc, int tile,
-                         long long at) -> bool {
+    auto find = [&](const Unit& u, const Seq& q, int tile) {
+      return tile < q.nc ? find_box<D>(p.c, u.b, tile * KT, q.len, box_rows) : TileBox{};
+    };
+    auto load_tile = [&](const CUtensorMap* ctx, const CUtensorMap* fresh, const Unit& u, int nc, int tile,
+                         const TileBox& box, uint32_t at) -> bool {
       const int st = (int)(at % NST);
       if (!__all_sync(0xffffffffu, mbar_wait(&s.kv_empty[st], ((at / NST) & 1) ^ 1, ab))) return false;
-      uint8_t* dst = s.kv[st];
       if (tile < nc) {
-        load_cache_tile<D>(dst, &s.kv_full[st], ctx, p.c, u.b, u.hk, tile * KT, len, box_rows, p.status);
-      } else if (lane == 0) {
-        mbar_expect_tx(&s.kv_full[st], new_box_rows * KB * 128);
+        load_cache_tile<D>(s.kv[st], &s.kv_full[st], ctx, p.c, box, u.hk, box_rows, p.status);
+      } else {
+        if (lane == 0) {
+          mbar_expect_tx(&s.kv_full[st], new_box_rows * KB * 128);
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          tma_load_4d(dst + kb * KT * 128, fresh, &s.kv_full[st], kb * 64, u.hk, (tile - nc) * KT, u.b);
+          for (int kb = 0; kb < KB; ++kb)
+            tma_load_4d(s.kv[st] + kb * KT * 128, fresh, &s.kv_full[st], kb * 64, u.hk, (tile - nc) * KT, u.b);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       return true;
     };
-    while (ok && w.next(p, rw, u)) {
-      if (u.empty) continue;
-      const int n = u.te - u.tb;
-      for (int t = 0; ok && t <= (u.two ? 1 : 0); ++t, ++nq) {
+    auto advance = [&](Unit& u) {  // to the next unit with something to load
+      while (w.next(p, rw, u))
+        if (!u.empty) return true;
+      return false;
+    };
+    bool more = advance(u);
+    TileBox box{};
+    if (more) box = find(u, w.s, u.tb);
+    while (more) {
+      const Unit v = u;
+      const Seq sq = w.s;
+      const int n = v.te - v.tb;
+      for (int t = 0; ok && t <= (v.two ? 1 : 0); ++t, ++nq) {
         const int slot = nq & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(&s.q_empty[slot], ((nq >> 1) & 1) ^ 1, ab));
         if (ok && lane == 0) {
-          const int rt = 2 * u.pair + t;
+          const int rt = 2 * v.pair + t;
           mbar_expect_tx(&s.q_full[slot], rw.gb * rw.tt * KB * 128);
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
             tma_load_4d(s.q[slot] + kb * BM * 128, &tm_q, &s.q_full[slot], kb * 64,
-                        u.hk * rw.G + rt % rw.gblk * rw.gb, rt / rw.gblk * rw.tt, u.b);
+                        v.hk * rw.G + rt % rw.gblk * rw.gb, rt / rw.gblk * rw.tt, v.b);
         }
         __syncwarp();
       }
-      // the order the products consume them in
+      more = advance(u);
+      // the order the products consume them in; the next tile's box is looked up
+      // before this one's loads wait for their buffers
+      TileBox prev{};
       for (int i = 0; ok && i <= n; ++i) {
-        if (u.two) {
+        const TileBox cur = box;
+        if (i + 1 < n)
+          box = find(v, sq, v.tb + i + 1);
+        else if (i + 1 == n && more)
+          box = find(u, w.s, u.tb);
+        if (v.two) {
           if (i == n) break;
-          if (!(ok = load_tile(&tm_k, &tm_kn, u, w.s.len, w.s.nc, u.tb + i, seq + seq_k(true, i)))) break;
-          ok = load_tile(&tm_v, &tm_vn, u, w.s.len, w.s.nc, u.tb + i, seq + seq_v(true, i, n));
+          if (!(ok = load_tile(&tm_k, &tm_kn, v, sq.nc, v.tb + i, cur, seq + seq_k(true, i)))) break;
+          ok = load_tile(&tm_v, &tm_vn, v, sq.nc, v.tb + i, cur, seq + seq_v(true, i, n));
         } else {
-          if (i < n && !(ok = load_tile(&tm_k, &tm_kn, u, w.s.len, w.s.nc, u.tb + i, seq + seq_k(false, i)))) break;
-          if (i > 0) ok = load_tile(&tm_v, &tm_vn, u, w.s.len, w.s.nc, u.tb + i - 1, seq + seq_v(false, i - 1, n));
+          if (i < n && !(ok = load_tile(&tm_k, &tm_kn, v, sq.nc, v.tb + i, cur, seq + seq_k(false, i)))) break;
+          if (i > 0) ok = load_tile(&tm_v, &tm_vn, v, sq.nc, v.tb + i - 1, prev, seq + seq_v(false, i - 1, n));
+          prev = cur;
         }
       }
-      if (ok) seq += 2 * n;
+      if (!ok) break;
+      seq += 2 * n;
     }
     if (s.abort_flag) {
       // leave no copy in flight into shared memory that is about to be released:
@@ -295,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16(BM, KT, 0, 0);  // Q: K-major, K tile: K-major
       constexpr uint32_t idesc_pv = idesc_bf16(BM, D, 0, 1);  // P: TMEM, V tile: MN-major
-      long long seq = 0;
+      uint32_t seq = 0;
       int nq = 0, units = 0;
       uint32_t done[2] = {0, 0};  // items of each stream whose P has been taken
       bool ok = true;
@@ -307,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = 0; ok && m <= items; ++m) {
           if (m < items) {
             const int i = u.two ? m >> 1 : m;
-            const long long at = seq + seq_k(u.two, i);
+            const uint32_t at = seq + seq_k(u.two, i);
             const int st = (int)(at % NST);
             if (!(ok = mbar_wait(&s.kv_full[st], (at / NST) & 1, ab))) break;
             tc_fence_after();
@@ -323,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (m > 0) {
             const int j = m - 1, i = u.two ? j >> 1 : j, str = j & 1;
-            const long long at = seq + seq_v(u.two, i, n);
+            const uint32_t at = seq + seq_v(u.two, i, n);
             const int st = (int)(at % NST);
             const bool first = j < 2;
             // the previous unit's O has been read
@@ -359,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t col_o = tmem + lane_off + 256;
     const float sc2 = p.scale * kLog2e;
     const int rows_in_tile = rw.gb * rw.tt;
-    long long seq = 0;
+    uint32_t seq = 0;
     uint32_t seen = 0;  // items of this stream
     int units = 0, singles = 0;
     bool ok = true;
@@ -383,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int keys = min(KT, (cached ? len : nr) - base);  // keys of this tile that exist
         if (keys < KT && (!u.two || str == 0)) {
           // V rows that do not exist take part with P = 0: they have to be finite
-          const long long at = seq + seq_v(u.two, i, n);
+          const uint32_t at = seq + seq_v(u.two, i, n);
           const int st = (int)(at % NST);
           ok = __all_sync(0xffffffffu, mbar_wait(&s.kv_full[st], (at / NST) & 1, ab));
           if (!ok) break;

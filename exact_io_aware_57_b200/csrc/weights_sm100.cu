@@ -20,7 +20,8 @@
 //   warps 4..7   sums of the odd steps
 //   warp 8       TMEM owner + single-thread tcgen05.mma issuer
 //   warp 9       TMA producer of K tiles, through the page table
-//   warps 10,11  Q rows (by the row list) and their -LSE into shared memory
+//   warps 10,11  producers of Q tiles (TMA, or copies by the row list) and of the
+//                rows' -LSE and visible ends
 //
 // TMEM: four score buffers of 128 columns, step s in buffer s & 3.
 #include <algorithm>
@@ -43,13 +44,15 @@ constexpr int NZ = 8;  // row-term ring
 template <int D>
 struct WeightsSmem {
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int NK = D == 128 ? 4 : 8, NQ = D == 128 ? 2 : 4;
-  alignas(1024) uint8_t k[NK][kTileBytes];
-  alignas(1024) uint8_t q[NQ][kTileBytes];
+  // K tiles [0, nk) and Q tiles [nk, NT) share the space: a launch of one row
+  // tile per head streams K past it, one of many streams Q past a K tile
+  static constexpr int NT = D == 128 ? 6 : 12;
+  static constexpr int kKeysFew = NT / 3, kKeysMany = 2 * NT / 3;  // nk of the two
+  alignas(1024) uint8_t tile[NT][kTileBytes];
   alignas(16) float z[NZ][BR];  // -LSE log2(e); -inf for a row that counts for nothing
   alignas(16) int last[NZ][BR];  // last slot the row sees
   float half[KT];  // the odd steps' sums of a unit
-  uint64_t k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ];
+  uint64_t t_full[NT], t_empty[NT];
   uint64_t z_full[NZ], z_empty[NZ], s_full[4], s_empty[4];
   uint64_t half_full, half_empty, drain;
   RunSmem<kThreads> run;
@@ -188,48 +191,85 @@ ATTN_DEVINL void reg_fence(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Sum of exponentials of N columns of a key: x = s * sc2 + z.
-template <int N>
-ATTN_DEVINL void add_columns(const uint32_t (&sr)[N], const float* z, const int* last, bool edge, int key, float sc2,
-                             float& a0, float& a1) {
+// Sum of exponentials of N columns of a key, x = s * sc2 + z in pairs (sc2 twice
+// in sc).  EDGE: a column whose row does not see the key, or does not count, adds
+// nothing whatever its score.
+template <bool EDGE, int N>
+ATTN_DEVINL void add_columns(const uint32_t (&sr)[N], const float* z, const int* last, int key, uint64_t sc,
+                             uint64_t& a0, uint64_t& a1) {
 #pragma unroll
   for (int e = 0; e < N; e += 4) {
-    const float4 zz = *reinterpret_cast<const float4*>(z + e);
-    float x0 = fmaf(__uint_as_float(sr[e]), sc2, zz.x), x1 = fmaf(__uint_as_float(sr[e + 1]), sc2, zz.y);
-    float x2 = fmaf(__uint_as_float(sr[e + 2]), sc2, zz.z), x3 = fmaf(__uint_as_float(sr[e + 3]), sc2, zz.w);
-    if (edge) {
+    const ulonglong2 zz = *reinterpret_cast<const ulonglong2*>(z + e);
+    const uint64_t s01 = pack_f32x2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+    const uint64_t s23 = pack_f32x2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3]));
+    float x0, x1, x2, x3;
+    unpack_f32x2(fma_f32x2(s01, sc, zz.x), x0, x1);
+    unpack_f32x2(fma_f32x2(s23, sc, zz.y), x2, x3);
+    if constexpr (EDGE) {
       const int4 ll = *reinterpret_cast<const int4*>(last + e);
       if (key > ll.x) x0 = -INFINITY;
       if (key > ll.y) x1 = -INFINITY;
       if (key > ll.z) x2 = -INFINITY;
       if (key > ll.w) x3 = -INFINITY;
     }
-    a0 += ex2(x0) + ex2(x2);
-    a1 += ex2(x1) + ex2(x3);
+    a0 = add_f32x2(a0, pack_f32x2(ex2(x0), ex2(x1)));
+    a1 = add_f32x2(a1, pack_f32x2(ex2(x2), ex2(x3)));
   }
+}
+
+// The same of a whole row tile in TMEM; a full one's next 32 columns are on
+// their way while 32 are summed.
+template <bool EDGE>
+ATTN_DEVINL float add_tile(uint32_t col, int width, const float* z, const int* last, int key, uint64_t sc) {
+  uint64_t a0 = 0, a1 = 0;  // a tile's own sums: short chains round less
+  if (width == BR) {
+    uint32_t sr[2][32];
+    tmem_ld32(col, sr[0]);
+    tmem_wait_ld();
+    reg_fence(sr[0]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c < 3) tmem_ld32(col + 32 * (c + 1), sr[(c + 1) & 1]);
+      add_columns<EDGE>(sr[c & 1], z + 32 * c, last + 32 * c, key, sc, a0, a1);
+      if (c < 3) {
+        tmem_wait_ld();
+        reg_fence(sr[(c + 1) & 1]);
+      }
+    }
+  } else {
+    for (int c = 0; c < width; c += 16) {
+      uint32_t sr[16];
+      tmem_ld16(col + c, sr);
+      tmem_wait_ld();
+      reg_fence(sr);
+      add_columns<EDGE>(sr, z + c, last + c, key, sc, a0, a1);
+    }
+  }
+  float x, y;
+  unpack_f32x2(add_f32x2(a0, a1), x, y);
+  return x + y;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    weights_kernel(const __grid_constant__ CUtensorMap tm_k, const WeightsParams p, const int box_rows) {
+    weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                   const WeightsParams p, const int box_rows) {
   using Smem = WeightsSmem<D>;
-  constexpr int NK = Smem::NK, NQ = Smem::NQ;
+  constexpr int NT = Smem::NT;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Rows rw = row_tiles(p.Hq, p.Hkv, p.max_rows);
+  const int width = min(BR, (rw.gb * rw.tt + 15) / 16 * 16);  // columns of a row tile
+  const int nk = (long long)p.max_rows * rw.G <= BR ? Smem::kKeysMany : Smem::kKeysFew, nq = NT - nk;
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    for (int i = 0; i < NK; ++i) {
-      mbar_init(&s.k_full[i], 1);
-      mbar_init(&s.k_empty[i], 1);
-    }
-    for (int i = 0; i < NQ; ++i) {
-      mbar_init(&s.q_full[i], 2);  // the two loading warps
-      mbar_init(&s.q_empty[i], 1);
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(&s.t_full[i], 1);
+      mbar_init(&s.t_empty[i], 1);
     }
     for (int i = 0; i < NZ; ++i) {
-      mbar_init(&s.z_full[i], 2);
+      mbar_init(&s.z_full[i], 1);
       mbar_init(&s.z_empty[i], 8);
     }
     for (int i = 0; i < 4; ++i) {
@@ -242,7 +282,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == kWarpMma) tmem_alloc(&s.tmem_base, kTmemCols);
-  if (warp == kWarpLoad && lane == 0) tma_prefetch_desc(&tm_k);
+  if (warp == kWarpLoad && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_q);
+  }
+  // columns that no load writes: zeros, so that their scores are finite
+  for (int i = threadIdx.x; i < nq * (width - rw.gb * rw.tt) * (D / 8); i += kThreads) {
+    const int c = i % (D / 8), r = rw.gb * rw.tt + i / (D / 8) % (width - rw.gb * rw.tt);
+    const int t = nk + i / (D / 8) / (width - rw.gb * rw.tt);
+    *reinterpret_cast<uint4*>(s.tile[t] + (c >> 3) * (BR * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
   tc_fence_before();
   const Run run = find_run<kThreads>(s.run, p.B, [&](int b) { return load_seq(p, rw, b).per_head * p.Hkv; });
   tc_fence_after();
@@ -254,108 +304,144 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpLoad) {
     // ===================================================== K producer
-    int i = 0;
-    bool ok = true;
-    for (; ok && w.next(p, rw, u); ++i) {
-      const int st = i % NK;
-      ok = __all_sync(0xffffffffu, mbar_wait(&s.k_empty[st], ((i / NK) & 1) ^ 1, ab));
-      if (ok)
-        load_cache_tile<D>(s.k[st], &s.k_full[st], &tm_k, p.c, u.b, u.hk, u.kt * KT, w.s.len, box_rows, p.status);
+    auto find = [&](const Unit& u) { return find_box<D>(p.c, u.b, u.kt * KT, w.s.len, box_rows); };
+    bool ok = true, more = w.next(p, rw, u);
+    TileBox box{};
+    if (more) box = find(u);
+    for (int i = 0; more; ++i) {
+      const int st = i % nk, hk = u.hk;
+      const TileBox cur = box;
+      // the slots' weights into L2, some tiles before their sums are ready
+      const int key = u.kt * KT + lane * 32;
+      if (p.weights && lane < 5 && key < w.s.len)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weights + ((long long)u.b * p.Hkv + hk) * p.cap + key));
+      if ((more = w.next(p, rw, u))) box = find(u);
+      ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[st], ((i / nk) & 1) ^ 1, ab));
+      if (!ok) break;
+      load_cache_tile<D>(s.tile[st], &s.t_full[st], &tm_k, p.c, cur, hk, box_rows, p.status);
     }
     if (s.abort_flag) {
       // leave no copy in flight into shared memory that is about to be released
-      for (int st = 0; st < NK; ++st) {
-        mbar_wait_drain(&s.k_full[st], 0, p.wait_limit / 64);
-        mbar_wait_drain(&s.k_full[st], 1, p.wait_limit / 64);
+      for (int st = 0; st < nk; ++st) {
+        mbar_wait_drain(&s.t_full[st], 0, p.wait_limit / 64);
+        mbar_wait_drain(&s.t_full[st], 1, p.wait_limit / 64);
       }
     }
   } else if (warp >= kWarpQ) {
     // ===================================================== Q rows
-    // Warp y loads rows [64 y, 64 y + 64) of each row tile: addresses a row per
-    // lane, then 16 bytes per lane and copy, in the 128-byte swizzle (chunk c of
-    // row r at chunk c ^ (r & 7)) that the products read.
+    // The two warps take row tiles in turn: -LSE and the last visible slot of
+    // each row, four rows a lane, and the rows themselves.  Rows in their own
+    // order come by TMA; listed rows by 16-byte copies into the same 128-byte
+    // swizzle (chunk c of row r at chunk c ^ (r & 7)).
     constexpr int CH = D / 8;  // 16-byte chunks per row
-    const int half = warp - kWarpQ;
-    int i = 0;  // row tiles loaded
+    int i = 0, issued = 0;     // row tiles passed; loads in flight by this warp
     bool ok = true;
     while (ok && w.next(p, rw, u)) {
       if (u.same_q) continue;
       for (int j = u.jb; ok && j < u.je; ++j, ++i) {
-        const int st = i % NQ, zt = i % NZ;
+        if ((i & 1) != warp - kWarpQ) continue;
+        const int st = nk + i % nq, zt = i % NZ;
         const int i0 = (u.first + j / rw.gblk) * rw.tt, g0 = j % rw.gblk * rw.gb;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s.z_empty[zt], ((i / NZ) & 1) ^ 1, ab) &&
-                                         mbar_wait(&s.q_empty[st], ((i / NQ) & 1) ^ 1, ab));
-        if (!ok) break;
-        const uint32_t qs = smem_u32(s.q[st]);
-#pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-          const int r = half * 64 + blk * 32 + lane, row = i0 + r / rw.gb, g = g0 + r % rw.gb;
-          long long src = -1;
-          float z = -INFINITY;
-          int last = -1;
+        long long src[4];
+        float z[4];
+        int last[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = x * 32 + lane, row = i0 + r / rw.gb, g = g0 + r % rw.gb;
+          src[x] = -1;
+          z[x] = -INFINITY;
+          last[x] = -1;
           if (r < rw.gb * rw.tt && row < w.s.cnt && g < rw.G) {
             const int t = p.rows ? __ldg(p.rows + (long long)u.b * p.max_rows + row) : row;
             if (t < 0 || t >= p.Nq) {
               atomicExch(p.status, ATTN_ERR_INVALID);
             } else {
               const int h = u.hk * rw.G + g;
-              src = (((long long)u.b * p.Nq + t) * p.Hq + h) * D;
+              src[x] = (((long long)u.b * p.Nq + t) * p.Hq + h) * D;
               const float lse = __ldg(p.lse + ((long long)u.b * p.Hq + h) * p.Nq + t);
-              z = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-              last = w.s.len - w.s.cnt + row;
+              z[x] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+              last[x] = w.s.len - w.s.cnt + row;
             }
           }
-          s.z[zt][r] = z;
-          s.last[zt][r] = last;
-          const char* base = static_cast<const char*>(p.q);
-#pragma unroll 4
-          for (int x = 0; x < CH; ++x) {
-            const int rr = x * (32 / CH) + lane / CH, c = lane % CH;  // row of the block, chunk of the row
-            const long long at = __shfl_sync(0xffffffffu, src, rr);
-            const int r2 = half * 64 + blk * 32 + rr;
-            const uint32_t dst = qs + (c >> 3) * (BR * 128) + r2 * 128 + (((c & 7) ^ (r2 & 7)) << 4);
-            // a row that counts for nothing is zeros
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                         "l"(base + (at < 0 ? 0 : at * 2 + c * 16)), "r"(at < 0 ? 0 : 16)
-                         : "memory");
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[st], ((i / nq) & 1) ^ 1, ab));
+        if (!ok) break;
+        if (!p.rows) {
+          if (lane == 0) {
+            mbar_expect_tx(&s.t_full[st], rw.gb * rw.tt * (D / 64) * 128);
+#pragma unroll
+            for (int kb = 0; kb < D / 64; ++kb)
+              tma_load_4d(s.tile[st] + kb * BR * 128, &tm_q, &s.t_full[st], kb * 64, u.hk * rw.G + g0, i0, u.b);
           }
+          __syncwarp();
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
+        issued = 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.z_empty[zt], ((i / NZ) & 1) ^ 1, ab));
+        if (!ok) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s.z[zt][x * 32 + lane] = z[x];
+          s.last[zt][x * 32 + lane] = last[x];
+        }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s.q_full[st]);
-          mbar_arrive(&s.z_full[zt]);
+        if (lane == 0) mbar_arrive(&s.z_full[zt]);
+        if (p.rows) {
+          const char* base = static_cast<const char*>(p.q);
+          const uint32_t qs = smem_u32(s.tile[st]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (x * 32 >= width) break;  // uniform
+#pragma unroll 1
+            for (int y = 0; y < CH; ++y) {
+              const int rr = y * (32 / CH) + lane / CH, c = lane % CH;  // row of the 32, chunk of the row
+              const long long at = __shfl_sync(0xffffffffu, src[x], rr);
+              const int r = x * 32 + rr;
+              const uint32_t dst = qs + (c >> 3) * (BR * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+              // a row that counts for nothing is zeros
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                           "l"(base + (at < 0 ? 0 : at * 2 + c * 16)), "r"(at < 0 ? 0 : 16)
+                           : "memory");
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.t_full[st]);
         }
+      }
+    }
+    if (s.abort_flag && issued && !p.rows) {
+      for (int st = nk; st < NT; ++st) {
+        mbar_wait_drain(&s.t_full[st], 0, p.wait_limit / 64);
+        mbar_wait_drain(&s.t_full[st], 1, p.wait_limit / 64);
       }
     }
   } else if (warp == kWarpMma) {
     // ===================================================== MMA issuer
     if (lane == 0) {
-      const int width = min(BR, (rw.gb * rw.tt + 15) / 16 * 16);
       const uint32_t idesc = idesc_bf16(KT, width, 0, 0);
       int i = 0, iq = -1, step = 0;
       bool ok = true;
       for (; ok && w.next(p, rw, u); ++i) {
-        const int kst = i % NK;
-        if (!(ok = mbar_wait(&s.k_full[kst], (i / NK) & 1, ab))) break;
+        const int kst = i % nk;
+        if (!(ok = mbar_wait(&s.t_full[kst], (i / nk) & 1, ab))) break;
         for (int j = u.jb; j < u.je; ++j, ++step) {
           if (!u.same_q) {
-            if (iq >= 0) mma_commit(&s.q_empty[iq % NQ]);  // the previous row tile has been used
+            if (iq >= 0) mma_commit(&s.t_empty[nk + iq % nq]);  // the previous row tile has been used
             ++iq;
-            if (!(ok = mbar_wait(&s.q_full[iq % NQ], (iq / NQ) & 1, ab))) break;
+            if (!(ok = mbar_wait(&s.t_full[nk + iq % nq], (iq / nq) & 1, ab))) break;
           }
           const int buf = step & 3;
           if (!(ok = mbar_wait(&s.s_empty[buf], ((step >> 2) & 1) ^ 1, ab))) break;
           tc_fence_after();
-          const uint32_t ka = smem_u32(s.k[kst]), qa = smem_u32(s.q[iq % NQ]);
+          const uint32_t ka = smem_u32(s.tile[kst]), qa = smem_u32(s.tile[nk + iq % nq]);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_ss(tmem + buf * BR, sdesc_sw128(ka + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024),
                    sdesc_sw128(qa + (kk >> 2) * (BR * 128) + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
           mma_commit(&s.s_full[buf]);
         }
-        if (ok) mma_commit(&s.k_empty[kst]);
+        if (ok) mma_commit(&s.t_empty[kst]);
       }
       // TMEM must be quiescent before it is released
       mma_commit(&s.drain);
@@ -365,8 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================================================== sums
     const int wg = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const float sc2 = p.scale * kLog2e;
-    const int width = min(BR, (rw.gb * rw.tt + 15) / 16 * 16);
+    const uint64_t sc = pack_f32x2(p.scale * kLog2e, p.scale * kLog2e);
     int step = 0, iz = -1, shared = 0;
     bool ok = true;
     while (ok && w.next(p, rw, u)) {
@@ -396,29 +481,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* z = s.z[iz % NZ];
         const int* last = s.last[iz % NZ];
         const uint32_t col = tmem + lane_off + buf * BR;
-        // rows from i0 on; the tile's last key is hidden from the first of them
+        // rows from i0 on: the tile's last key is hidden from the first of them,
+        // or the last of them do not count
         const int i0 = (u.first + j / rw.gblk) * rw.tt;
-        const bool edge = u.kt * KT + KT - 1 > w.s.len - w.s.cnt + i0;
-        float a0 = 0.f, a1 = 0.f;  // a tile's own sums: short chains round less
-        int c = 0;
-        for (; c + 32 <= width; c += 32) {
-          uint32_t sr[32];
-          tmem_ld32(col + c, sr);
-          tmem_wait_ld();
-          reg_fence(sr);
-          add_columns(sr, z + c, last + c, edge, key, sc2, a0, a1);
-        }
-        if (c < width) {
-          uint32_t sr[16];
-          tmem_ld16(col + c, sr);
-          tmem_wait_ld();
-          reg_fence(sr);
-          add_columns(sr, z + c, last + c, edge, key, sc2, a0, a1);
-        }
+        const bool edge = u.kt * KT + KT - 1 > w.s.len - w.s.cnt + i0 || i0 + rw.tt > w.s.cnt || rw.gblk > 1;
+        const float part = edge ? add_tile<true>(col, width, z, last, key, sc)
+                                : add_tile<false>(col, width, z, last, key, sc);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.s_empty[buf]);
-        sum += a0 + a1;
+        sum += part;
       }
       if (!ok) break;
       if (n > 1) {  // both warpgroups took steps
@@ -465,13 +537,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The first blocks add the parts of the units that a cut divides, in CTA order;
-// when out is another buffer than weights, all blocks copy the slots that no
-// unit covers (behind each sequence's end).
-__global__ void __launch_bounds__(KT) weights_finish_kernel(const WeightsParams p, const int ctas) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// Blocks (c < ctas, 0) add the parts of the unit whose first part CTA c holds, in
+// CTA order.  When out is another buffer than weights, block (u, y) copies the
+// y-th run of the slots of (sequence, KV head) u that no unit covers (behind the
+// sequence's end); it need not wait for that.
+constexpr int kFinish = 256, kCopyRun = 8 * kFinish;
+
+__global__ void __launch_bounds__(kFinish) weights_finish_kernel(const WeightsParams p, const int ctas) {
   const int r = threadIdx.x;
-  if ((int)blockIdx.x < ctas) {
+  if (p.weights != p.out && blockIdx.x < (unsigned)(p.B * p.Hkv)) {
+    int len, cnt;
+    const int b = blockIdx.x / p.Hkv;
+    // a sequence that is not acceptable is left as it is
+    if (cache_len(p.c, b, p.cap, p.status, len) && row_count(p.row_lens, b, p.max_rows, p.status, cnt)) {
+      const int from = cnt > 0 ? len : 0, j0 = blockIdx.y * kCopyRun + r;
+      const float* src = p.weights ? p.weights + (long long)blockIdx.x * p.cap : nullptr;
+      float* dst = p.out + (long long)blockIdx.x * p.cap;
+      float x[kCopyRun / kFinish];
+#pragma unroll
+      for (int i = 0; i < kCopyRun / kFinish; ++i) {
+        const int j = j0 + i * kFinish;
+        x[i] = src && j >= from && j < p.cap ? src[j] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kCopyRun / kFinish; ++i) {
+        const int j = j0 + i * kFinish;
+        if (j >= from && j < p.cap) dst[j] = x[i];
+      }
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x < ctas && blockIdx.y == 0 && r < KT) {
     const WeightsCut cut = p.cuts[blockIdx.x];
     const int key = cut.kt * KT + r;
     if (cut.more > 0 && key < p.c.lens[cut.b]) {
@@ -480,15 +576,6 @@ __global__ void __launch_bounds__(KT) weights_finish_kernel(const WeightsParams 
       const long long at = ((long long)cut.b * p.Hkv + cut.hk) * p.cap + key;
       p.out[at] = (p.weights ? p.weights[at] : 0.f) + sum;
     }
-  }
-  if (p.weights == p.out) return;
-  for (long long u = blockIdx.x; u < (long long)p.B * p.Hkv; u += gridDim.x) {
-    int len, cnt;
-    const int b = (int)(u / p.Hkv);
-    // a sequence that is not acceptable is left as it is
-    if (!cache_len(p.c, b, p.cap, p.status, len) || !row_count(p.row_lens, b, p.max_rows, p.status, cnt)) continue;
-    for (int j = (cnt > 0 ? len : 0) + r; j < p.cap; j += KT)
-      p.out[u * p.cap + j] = p.weights ? p.weights[u * p.cap + j] : 0.f;
   }
 }
 
@@ -504,16 +591,25 @@ int launch_t(const WeightsParams& p, cudaStream_t st) {
   const uint32_t kb[4] = {64, 1, (uint32_t)box, 1};
   int rc;
   if ((rc = encode_tmap_bf16(&mk, p.c.k, 4, kd, ks, kb))) return rc;
+  const Rows rw = row_tiles(p.Hq, p.Hkv, p.max_rows);
+  CUtensorMap mq;
+  const uint64_t rq = (uint64_t)p.Hq * D * 2;
+  const uint64_t qd[4] = {D, (uint64_t)p.Hq, (uint64_t)p.Nq, (uint64_t)p.B}, qs[3] = {D * 2, rq, rq * p.Nq};
+  const uint32_t qb[4] = {64, (uint32_t)rw.gb, (uint32_t)rw.tt, 1};
+  std::memset(&mq, 0, sizeof(mq));
+  if (!p.rows && (rc = encode_tmap_bf16(&mq, p.q, 4, qd, qs, qb))) return rc;
   const size_t smem = sizeof(WeightsSmem<D>) + 1024;
   static_assert(sizeof(WeightsSmem<D>) + 1024 <= 232448, "shared memory");
   if (cudaFuncSetAttribute(weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
   const int ctas = sm_count();
-  weights_kernel<D><<<ctas, kThreads, smem, st>>>(mk, p, box);
+  weights_kernel<D><<<ctas, kThreads, smem, st>>>(mk, mq, p, box);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::max<long long>(ctas, std::min<long long>((long long)p.B * p.Hkv, 4ll * ctas)));
-  cfg.blockDim = dim3(KT);
+  cfg.gridDim = p.weights == p.out ? dim3((unsigned)ctas)
+                                   : dim3((unsigned)std::max((long long)ctas, (long long)p.B * p.Hkv),
+                                          (unsigned)((p.cap + kCopyRun - 1) / kCopyRun));
+  cfg.blockDim = dim3(kFinish);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
