@@ -15,15 +15,6 @@ struct CacheView {
   int num_pages, page_size, max_pages;  // max_pages 1 without a table
 };
 
-// Slots per TMA box: a box never straddles a page (the largest power of two that
-// divides it; a table's pages are multiples of 8).
-inline int cache_box_rows(const CacheView& c) {
-  int box = 128;
-  if (c.table)
-    while (c.page_size % box) box >>= 1;
-  return box;
-}
-
 ATTN_DEVINL long long cache_capacity(const CacheView& c) { return (long long)c.max_pages * c.page_size; }
 
 // Slots of sequence b in use; false (and ATTN_ERR_INVALID in the status word)
@@ -61,121 +52,191 @@ ATTN_DEVINL long long cache_row(const CacheView& c, int b, int s, int* status) {
 }
 
 // ---- equal runs.  The work of a launch is a line of `total` steps, sequence b
-// owning cost(b) of them; CTA c takes the steps [run0, run1), its share when at
-// most `total` CTAs take part, and its run begins `off` steps into sequence b.
+// owning cost(b) of them.  It is cut into equal runs, one per worker; a block has
+// LANES workers, blockIdx + lane * gridDim, so that with few steps every block
+// has its first worker busy.  At most `total` workers take part: worker w then
+// takes the steps [run0, run1), beginning `off` steps into sequence b.
 struct Run {
-  long long total, run0, run1, off;
-  int ctas, b;
-};
-
-template <int THREADS>
-struct RunSmem {
-  long long sum[THREADS / 32];
-  long long off;
+  long long run0, run1, off;
   int b;
 };
 
-// All THREADS threads of the block take part; the block is synchronised on return.
-template <int THREADS, class Cost>
-ATTN_DEVINL Run find_run(RunSmem<THREADS>& s, int B, Cost cost) {
+template <int LANES>
+struct Runs {
+  long long total;
+  int workers;
+  Run lane[LANES];
+};
+
+template <int THREADS, int LANES>
+struct RunSmem {
+  long long sum[THREADS / 32];
+  Runs<LANES> runs;  // the result
+};
+
+ATTN_DEVINL long long run_begin(long long total, int workers, int w) {
+  // 32-bit products and quotients where they do
+  if (total < (1 << 20) && workers < (1 << 11)) return (unsigned)w * (unsigned)total / (unsigned)workers;
+  return w * total / workers;
+}
+
+// Leaves the block's runs in s.runs.  All THREADS threads of the block take part;
+// the block is synchronised on return.
+template <int THREADS, int LANES, class Cost>
+ATTN_DEVINL void find_runs(RunSmem<THREADS, LANES>& s, int B, Cost cost) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long mine = 0;
-  for (int b = threadIdx.x; b < B; b += THREADS) mine += cost(b);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s.sum[warp] = mine;
-  __syncthreads();
-  Run r;
-  r.total = 0;
-#pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) r.total += s.sum[i];
-  r.ctas = (int)min((long long)gridDim.x, r.total);
-  r.run0 = r.ctas ? min((int)blockIdx.x, r.ctas) * r.total / r.ctas : 0;
-  r.run1 = r.ctas ? min((int)blockIdx.x + 1, r.ctas) * r.total / r.ctas : 0;
-  r.b = 0;
-  r.off = 0;
-  if (r.run1 == r.run0) return r;  // uniform
-  long long before = 0;
-  for (int b0 = 0; b0 < B && before <= r.run0; b0 += THREADS) {
-    const int b = b0 + threadIdx.x;
-    const long long w = b < B ? cost(b) : 0;
-    long long x = w;
+  // inclusive sum over the block's threads; all: their total
+  auto scan = [&](long long x, long long& all) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    __syncthreads();
     if (lane == 31) s.sum[warp] = x;
     __syncthreads();
-    long long all = 0;
+    all = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
       if (i < warp) x += s.sum[i];
       all += s.sum[i];
     }
-    const long long lo = before + x - w;
-    if (lo <= r.run0 && r.run0 < lo + w) {
-      s.b = b;
-      s.off = r.run0 - lo;
-    }
-    before += all;
+    return x;
+  };
+  long long w = (int)threadIdx.x < B ? cost(threadIdx.x) : 0, all;
+  long long x = scan(w, all);
+  long long total = all;
+  for (int b0 = THREADS; b0 < B; b0 += THREADS) {
+    __syncthreads();
+    const int b = b0 + threadIdx.x;
+    scan(b < B ? cost(b) : 0, all);
+    total += all;
+  }
+  const int workers = (int)min((long long)gridDim.x * LANES, total);
+  long long run0[LANES];
+#pragma unroll
+  for (int l = 0; l < LANES; ++l) {
+    const int me = blockIdx.x + l * gridDim.x;
+    run0[l] = me < workers ? run_begin(total, workers, me) : -1;
+    if (threadIdx.x == 0) s.runs.lane[l] = Run{0, 0, 0, 0};
   }
   __syncthreads();
-  r.b = s.b;
-  r.off = s.off;
-  return r;
+  auto look = [&](int b, long long lo) {
+#pragma unroll
+    for (int l = 0; l < LANES; ++l)
+      if (lo <= run0[l] && run0[l] < lo + w)
+        s.runs.lane[l] = Run{run0[l], run_begin(total, workers, blockIdx.x + l * gridDim.x + 1), run0[l] - lo, b};
+  };
+  if (B <= THREADS) {
+    look(threadIdx.x, x - w);
+  } else {
+    long long before = 0;
+    for (int b0 = 0; b0 < B; b0 += THREADS) {
+      __syncthreads();
+      const int b = b0 + threadIdx.x;
+      w = b < B ? cost(b) : 0;
+      x = scan(w, all);
+      look(b, before + x - w);
+      before += all;
+    }
+  }
+  if (threadIdx.x == 0) {
+    s.runs.total = total;
+    s.runs.workers = workers;
+  }
+  __syncthreads();
 }
 
-// CTAs behind the one whose run ends at run1 that a unit reaches into when it
-// still has `rest` steps there.
-ATTN_DEVINL int run_parts(const Run& r, long long rest) {
-  int c = blockIdx.x + 1;
-  while ((c + 1ll) * r.total / r.ctas < r.run1 + rest) ++c;
-  return c - (int)blockIdx.x;
+// Workers behind worker w, whose run ends at run1, into which the `rest` steps behind
+// it reach.
+ATTN_DEVINL int run_parts(long long total, int workers, int w, long long run1, long long rest) {
+  int c = w + 1;
+  while (run_begin(total, workers, c + 1) < run1 + rest) ++c;
+  return c - w;
 }
 
-// Where a lane's box of a 128-key tile of cached slots lies: boxes of box_rows
-// slots that never straddle a page, lane = (piece of the tile, 64-element block).
-// Looked up a tile ahead of its load, so that no load waits for the page table.
-struct TileBox {
-  int page, row, live;  // live: boxes of the tile that begin below the length
+// ---- tiles of 128 slots in shared memory.  Groups of 8 slots, and in a group the
+// 64-element blocks of the rows one after the other, 8 lines of 128 bytes each
+// (the 128-byte swizzle's unit), so that one TMA box of any multiple of 8 slots
+// brings whole rows:
+//   slot s, block kb: (s / 8) * group + kb * 1024 + s % 8 * 128,  group = d * 16.
+template <int D>
+constexpr int kGroupBytes = D * 16;
+
+// A tensor map of rows [.., h_kv, d] as {64, row, block of a row, group, page}:
+// coordinates (0, row, hk * d / 64, group, page).  Grouped, a row is one of 8 and
+// boxes are `rows` slots; else a row is any, boxes are 8 slots and groups are
+// not used (rows that are no multiple of 8: a group must not pass the last one).
+struct TileForm {
+  int rows;  // slots per box
+  int grouped;
 };
 
-template <int D>
-ATTN_DEVINL TileBox find_box(const CacheView& c, int b, int base, int len, int box_rows) {
+// Where a lane's box of a tile lies, a lane per box.  Looked up a tile ahead of
+// its load, so that no load waits for the page table.
+struct TileBox {
+  int row, group, page, live;  // live: boxes of the tile that begin below the length
+};
+
+ATTN_DEVINL TileBox find_box(const CacheView& c, const TileForm& f, int b, int base, int len) {
   const int lane = threadIdx.x & 31;
   TileBox t;
-  t.live = min(128 / box_rows, (len - base + box_rows - 1) / box_rows);
-  const int piece = lane / (D / 64), slot = base + piece * box_rows;
+  t.live = min(128 / f.rows, (len - base + f.rows - 1) / f.rows);
+  int slot = base + lane * f.rows;
   t.page = b;
-  t.row = slot;
-  if (c.table && piece < t.live) {
+  if (c.table && lane < t.live) {
     t.page = __ldg(c.table + (long long)b * c.max_pages + slot / c.page_size);
-    t.row = slot % c.page_size;
+    slot %= c.page_size;
   }
+  t.row = f.grouped ? 0 : slot;
+  t.group = f.grouped ? slot / 8 : 0;
   return t;
 }
 
-// Load that tile of KV head hk into dst (64-element blocks of 128 rows each), all
-// lanes of a warp taking part.  Rows behind its last live box are not written.
+// Load the tile of KV head hk into dst, all lanes of a warp taking part.  Slots
+// behind the last live box are not written.
 template <int D>
-ATTN_DEVINL void load_cache_tile(uint8_t* dst, uint64_t* bar, const CUtensorMap* map, const CacheView& c,
-                                 const TileBox& t, int hk, int box_rows, int* status) {
-  constexpr int KB = D / 64;
+ATTN_DEVINL void load_tile(uint8_t* dst, uint64_t* bar, const CUtensorMap* map, const TileForm& f, const TileBox& t,
+                           int hk, int pages, int* status) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0) mbar_expect_tx(bar, t.live * box_rows * KB * 128);
+  if (lane == 0) mbar_expect_tx(bar, t.live * f.rows * D * 2);
   __syncwarp();
-  const int piece = lane / KB, kb = lane % KB;
-  if (piece < t.live) {
+  if (lane < t.live) {
     int page = t.page;
-    if (page < 0 || page >= c.num_pages) {
+    if (page < 0 || page >= pages) {
       atomicExch(status, ATTN_ERR_INVALID);
-      page = c.num_pages;  // outside the tensor: zeros are loaded
+      page = pages;  // outside the tensor: zeros are loaded
     }
-    tma_load_4d(dst + kb * 128 * 128 + piece * box_rows * 128, map, bar, kb * 64, hk, t.row, page);
+    tma_load_5d(dst + lane * (f.rows / 8) * kGroupBytes<D>, map, bar, 0, t.row, hk * (D / 64), t.group, page);
   }
   __syncwarp();
+}
+
+// Zero slot r of a tile.
+template <int D>
+ATTN_DEVINL void zero_slot(uint8_t* tile, int r) {
+#pragma unroll
+  for (int kb = 0; kb < D / 64; ++kb)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(tile + (r >> 3) * kGroupBytes<D> + kb * 1024 + (r & 7) * 128 + i * 16) =
+          make_uint4(0, 0, 0, 0);
+}
+
+// Descriptors of a tile for the tensor cores: as rows of K (16 elements of a row
+// per instruction), and as rows of V (16 slots per instruction; with d = 64 every
+// further block of columns is the first again).
+template <int D>
+ATTN_DEVINL uint64_t k_tile_desc(const uint8_t* tile) {
+  return sdesc_sw128(smem_u32(tile), 16, kGroupBytes<D>);
+}
+ATTN_DEVINL uint64_t k_tile_step(uint64_t desc, int kk) { return sdesc_at(desc, (kk >> 2) * 1024 + (kk & 3) * 32); }
+template <int D>
+ATTN_DEVINL uint64_t v_tile_desc(const uint8_t* tile) {
+  return sdesc_sw128(smem_u32(tile), D > 64 ? 1024 : 0, kGroupBytes<D>);
+}
+template <int D>
+ATTN_DEVINL uint64_t v_tile_step(uint64_t desc, int kk) {
+  return sdesc_at(desc, kk * 2 * kGroupBytes<D>);
 }
 
 }  // namespace attn

@@ -160,15 +160,21 @@ int launch_wait_selftest(long long limit_cycles, cudaStream_t st);
 int launch_ex2_selftest(const float* x, float* y, long long n, cudaStream_t st);
 
 // ------------------------------------------------- key/value cache (cache.cuh)
-// A unit of the bf16 tree attention that a cut between CTAs divides:
-// pair2 = 2 * pair + (two row tiles); `more` later parts follow the first one
-// (0: the CTA's run begins no unit that a cut divides).
+// How the query rows of one (sequence, KV head) make up tiles of the bf16 paths:
+// tt tokens x gb of the group's G heads each, gblk blocks of heads, `tiles` in all.
+struct RowTiles {
+  int G, gb, tt, gblk, tiles;
+};
+
+// A unit of the bf16 tree attention that a cut between workers divides: `more`
+// later parts follow the first one (0: the worker's run begins no such unit).
 struct TreeCut {
-  int b, hk, pair2, more;
+  int b, hk, pair, tiles, more;
 };
 // Tree attention: row t of sequence b sees its cached slots and the drafted
 // keys j with bit j of its mask row (without a mask: j <= t).
 struct TreeParams {
+  RowTiles rw;  // bf16 path
   const void *q, *k_new, *v_new;  // k_new / v_new null: no drafted keys
   CacheView c;
   const unsigned long long* mask;  // [mask_words] per row, or null
@@ -182,10 +188,20 @@ struct TreeParams {
   int num_splits;
   float *o_part, *lse_part;  // fp32 path: as SplitKV's; bf16 path: raw O, and (m, l) pairs
   int part_tiles;            // bf16 path: row tiles of a partial (1 or 2)
-  TreeCut* cuts;             // one per CTA
+  TreeCut* cuts;             // one per worker
   int* status;
   long long wait_limit;
 };
+// Tensor maps of a launch, and the forms of the cache's and the new keys' tiles.
+struct TreeMaps {
+  CUtensorMap q, k, v, k_new, v_new;
+  TileForm form, new_form;
+};
+// Map and form of tiles of a cache's rows, and of rows [batch, n, h_kv, d].
+int cache_tile_map(CUtensorMap* map, TileForm* form, const CacheView& c, const void* base, int Hkv, int D);
+int rows_tile_map(CUtensorMap* map, TileForm* form, const void* base, int Hkv, int D, int n, int batch);
+// Up to 16 query rows per (sequence, KV head): two workers per CTA.
+int launch_tree_few(const TreeParams& p, const TreeMaps& m, cudaStream_t st);
 size_t tree_sm100_workspace(int Hq, int Hkv, int Nq, int D);
 int launch_tree_sm100(TreeParams p, void* workspace, cudaStream_t st);
 int tree_f32_splits(int B, int Hq, int Hkv, int Nq, long long capacity);
@@ -198,6 +214,7 @@ struct WeightsCut {
   int b, hk, kt, more;
 };
 struct WeightsParams {
+  RowTiles rw;  // bf16 path
   const void* q;
   const float* lse;
   CacheView c;

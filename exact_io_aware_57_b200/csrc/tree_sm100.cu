@@ -1,8 +1,6 @@
-// Tree attention over a key/value cache on sm_100a tensor cores (bf16).
-//
-// A few new tokens per sequence (one, a chunk, a drafted tree) attend to a long
-// cache: every K/V row is read once for the few query rows of its sequence and
-// KV head, so the kernel is bound by HBM and is built to stream.
+// Tree attention over a key/value cache on sm_100a tensor cores (bf16) for more than
+// 16 query rows per (sequence, KV head), and the combination of partials that both
+// kernels leave (tree_few_sm100.cu has up to 16 rows).
 //
 // Rows.  The query rows of one (sequence, KV head) are all (token t, head g of
 // the group), packed as tiles of up to 128 rows: `tt` tokens x `gb` heads, row
@@ -42,14 +40,13 @@
 #include <algorithm>
 #include <cstring>
 
-#include "cache.cuh"
-#include "kernels.h"
+#include "tree.cuh"
 
 namespace attn {
 
 namespace {
 
-constexpr int KT = 128;  // keys per tile
+constexpr int KT = kTreeKeys;  // keys per tile
 constexpr int BM = 128;  // rows per tile
 constexpr int kWarpMma = 8, kWarpLoad = 9;
 constexpr int kThreads = 320;
@@ -68,96 +65,9 @@ struct TreeSmem {
   uint64_t kv_full[NST], kv_empty[NST];
   uint64_t s_full[2], p_full[2];
   uint64_t o_done, o_free, ml_full, drain;
-  RunSmem<kThreads> run;
+  RunSmem<kThreads, 1> run;
   uint32_t tmem_base;
   int abort_flag;
-};
-
-// Row tiles of a launch: tt tokens x gb heads each, gblk blocks of heads.
-struct Rows {
-  int G, gb, tt, gblk, tiles;  // tiles = token blocks * gblk
-};
-
-__host__ __device__ inline Rows row_tiles(int Hq, int Hkv, int Nq) {
-  Rows r;
-  r.G = Hq / Hkv;
-  r.gb = r.G < BM ? r.G : BM;
-  const int fit = BM / r.gb;
-  r.tt = fit < Nq ? fit : Nq;
-  r.gblk = (r.G + r.gb - 1) / r.gb;
-  r.tiles = (Nq + r.tt - 1) / r.tt * r.gblk;
-  return r;
-}
-
-// One sequence's share of the work: per KV head `active` units of n tiles, then
-// the units whose rows are all padding (one empty step each).
-struct Seq {
-  int len, nr, nc, n, row_tiles, active;
-  long long per_head;
-};
-
-ATTN_DEVINL Seq load_seq(const TreeParams& p, const Rows& rw, int b) {
-  Seq s;
-  if (!cache_len(p.c, b, 1ll << 31, p.status, s.len) || !row_count(p.row_lens, b, p.Nq, p.status, s.nr))
-    s.len = s.nr = 0;
-  s.nc = (s.len + KT - 1) / KT;
-  s.n = s.nc + (p.k_new ? (s.nr + KT - 1) / KT : 0);
-  s.row_tiles = s.n > 0 ? (s.nr + rw.tt - 1) / rw.tt * rw.gblk : 0;
-  s.active = (s.row_tiles + 1) / 2;
-  s.per_head = (long long)s.active * s.n + ((rw.tiles + 1) / 2 - s.active);
-  return s;
-}
-
-// A CTA's run of tiles, unit by unit.
-struct Unit {
-  int b, hk, pair;      // row tiles 2 pair, 2 pair + 1
-  int tb, te, n;        // tiles [tb, te) of n
-  bool two, empty;      // two row tiles; no row of it sees anything
-};
-
-struct Walk {
-  int b, hk;
-  long long off, left;  // position inside (b, hk); tiles left in the run
-  Seq s;
-
-  ATTN_DEVINL void begin(const TreeParams& p, const Rows& rw, int b0, long long off0, long long run) {
-    b = b0;
-    left = run;
-    if (left <= 0) return;
-    s = load_seq(p, rw, b);
-    hk = (int)(off0 / s.per_head);
-    off = off0 % s.per_head;
-  }
-  ATTN_DEVINL bool next(const TreeParams& p, const Rows& rw, Unit& u) {
-    if (left <= 0) return false;
-    if (off == s.per_head) {
-      off = 0;
-      if (++hk == p.Hkv) {
-        hk = 0;
-        s = load_seq(p, rw, ++b);
-      }
-    }
-    u.b = b;
-    u.hk = hk;
-    const long long busy = (long long)s.active * s.n;
-    if (off < busy) {
-      u.pair = (int)(off / s.n);
-      u.tb = (int)(off % s.n);
-      u.n = s.n;
-      u.te = (int)min((long long)s.n, u.tb + left);
-      u.two = 2 * u.pair + 1 < s.row_tiles;
-      u.empty = false;
-    } else {
-      u.pair = s.active + (int)(off - busy);
-      u.tb = 0;
-      u.te = u.n = 1;
-      u.two = false;
-      u.empty = true;
-    }
-    off += u.te - u.tb;
-    left -= u.te - u.tb;
-    return true;
-  }
 };
 
 // Position of K / V tile i of a unit of `n` tiles in the order of its loads
@@ -165,10 +75,85 @@ struct Walk {
 ATTN_DEVINL int seq_k(bool two, int i) { return two ? 2 * i : (i == 0 ? 0 : 2 * i - 1); }
 ATTN_DEVINL int seq_v(bool two, int i, int n) { return two ? 2 * i + 1 : (i == n - 1 ? 2 * n - 1 : 2 * i + 2); }
 
-template <int N>
-ATTN_DEVINL void reg_fence(uint32_t (&r)[N]) {
+// One key tile of one row: scores from TMEM, the reference maximum m moved when
+// the tile's exceeds it by more than 2^8, P over the scores.  EDGE: keys whose
+// bit is clear are hidden, whatever their score.
+struct SoftmaxStep {
+  float m, alpha, sum;  // alpha = 2^(old m - m); sum of the tile's P
+};
+
+template <bool EDGE>
+ATTN_DEVINL SoftmaxStep softmax_tile(uint32_t col_s, uint64_t sc2, float m, const uint32_t (&bits)[4]) {
+  // half a row of scores, x = s * scale * log2(e) in pairs
+  uint64_t x[KT / 4];
+  auto load_half = [&](int half) {
+    uint32_t sr[KT / 2];
+    tmem_ld32(col_s + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+    tmem_ld32(col_s + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+    tmem_wait_ld();
+    reg_fence(sr);
+    const uint32_t lo = half ? bits[2] : bits[0], hi = half ? bits[3] : bits[1];
 #pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+    for (int c = 0; c < KT / 2; c += 2) {
+      uint64_t y = fma_f32x2(pack_f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, 0ull);
+      if constexpr (EDGE) {
+        float y0, y1;
+        unpack_f32x2(y, y0, y1);
+        const uint32_t b = (c < 32 ? lo : hi) >> (c & 31);
+        y = pack_f32x2(b & 1u ? y0 : -INFINITY, b & 2u ? y1 : -INFINITY);
+      }
+      x[c / 2] = y;
+    }
+  };
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+  auto max_half = [&]() {
+#pragma unroll
+    for (int c = 0; c < KT / 4; c += 2) {
+      float a, b, d, e;
+      unpack_f32x2(x[c], a, b);
+      unpack_f32x2(x[c + 1], d, e);
+      mx0 = fmaxf(mx0, fmaxf(a, b));
+      mx1 = fmaxf(mx1, fmaxf(d, e));
+    }
+  };
+  // the second half is read twice, which takes half the registers of one read
+  // (128 scores at once spill); P of the first half overwrites only scores that
+  // are in registers
+  load_half(1);
+  max_half();
+  load_half(0);
+  max_half();
+  SoftmaxStep r;
+  const float mx = fmaxf(mx0, mx1);
+  const bool move = mx > m + kRescaleThreshold;
+  r.m = move ? mx : m;
+  r.alpha = move ? ex2(m - r.m) : 1.f;
+  const float neg_m = r.m == -INFINITY ? 0.f : -r.m;
+  const uint64_t nm = pack_f32x2(neg_m, neg_m);
+  uint64_t sum0 = 0, sum1 = 0;
+  auto store_half = [&](int half) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float y0, y1;
+        unpack_f32x2(add_f32x2(x[c * 16 + e], nm), y0, y1);
+        const float p0 = ex2(y0), p1 = ex2(y1);
+        uint64_t& sum = e & 1 ? sum1 : sum0;
+        sum = add_f32x2(sum, pack_f32x2(p0, p1));
+        pk[e] = pack_bf16(p0, p1);  // the product's operand; the sum l keeps 32 bits
+      }
+      tmem_st16(col_s + half * 32 + c * 16, pk);
+    }
+  };
+  store_half(0);
+  load_half(1);
+  store_half(1);
+  float y0, y1;
+  unpack_f32x2(add_f32x2(sum0, sum1), y0, y1);
+  r.sum = y0 + y1;
+  return r;
 }
 
 ATTN_DEVINL void store_bf16_32(__nv_bfloat16* dst, const float (&x)[32]) {
@@ -183,15 +168,15 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
-                const __grid_constant__ CUtensorMap tm_vn, const TreeParams p, const int box_rows,
-                const int new_box_rows) {
+                const __grid_constant__ CUtensorMap tm_vn, const TreeParams p, const TileForm form,
+                const TileForm new_form) {
   using Smem = TreeSmem<D>;
   constexpr int NST = Smem::NST;
   constexpr int KB = D / 64;  // 128-byte blocks per row
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Rows rw = row_tiles(p.Hq, p.Hkv, p.Nq);
+  const RowTiles& rw = p.rw;
 
   // ---- setup
   if (threadIdx.x == 0) {
@@ -220,40 +205,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
-  const Run run = find_run<kThreads>(s.run, p.B, [&](int b) { return load_seq(p, rw, b).per_head * p.Hkv; });
+  find_runs<kThreads, 1>(s.run, p.B, [&](int b) { return tree_seq(p, rw, b).per_head * p.Hkv; });
   tc_fence_after();
+  const Runs<1>& runs = s.run.runs;
+  const Run& run = runs.lane[0];
   const uint32_t tmem = s.tmem_base;
   const Abort ab{&s.abort_flag, p.status, p.wait_limit};
-  Walk w;
-  w.begin(p, rw, run.b, run.off, run.run1 - run.run0);
-  Unit u{};
+  TreeWalk w;
+  w.begin(p, rw, run);
+  TreeUnit u{};
 
   if (warp == kWarpLoad) {
     // ===================================================== TMA producer
     uint32_t seq = 0;  // K/V tiles loaded
     int nq = 0;         // Q tiles loaded
     bool ok = true;
-    auto find = [&](const Unit& u, const Seq& q, int tile) {
-      return tile < q.nc ? find_box<D>(p.c, u.b, tile * KT, q.len, box_rows) : TileBox{};
-    };
-    auto load_tile = [&](const CUtensorMap* ctx, const CUtensorMap* fresh, const Unit& u, int nc, int tile,
-                         const TileBox& box, uint32_t at) -> bool {
+    auto find = [&](const TreeUnit& u, const TreeSeq& q, int tile) { return tree_box(p, form, new_form, q, u.b, tile); };
+    auto load = [&](const CUtensorMap* ctx, const CUtensorMap* fresh, const TreeUnit& u, int nc, int tile,
+                    const TileBox& box, uint32_t at) -> bool {
       const int st = (int)(at % NST);
       if (!__all_sync(0xffffffffu, mbar_wait(&s.kv_empty[st], ((at / NST) & 1) ^ 1, ab))) return false;
-      if (tile < nc) {
-        load_cache_tile<D>(s.kv[st], &s.kv_full[st], ctx, p.c, box, u.hk, box_rows, p.status);
-      } else {
-        if (lane == 0) {
-          mbar_expect_tx(&s.kv_full[st], new_box_rows * KB * 128);
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-            tma_load_4d(s.kv[st] + kb * KT * 128, fresh, &s.kv_full[st], kb * 64, u.hk, (tile - nc) * KT, u.b);
-        }
-        __syncwarp();
-      }
+      if (tile < nc)
+        load_tile<D>(s.kv[st], &s.kv_full[st], ctx, form, box, u.hk, p.c.num_pages, p.status);
+      else
+        load_tile<D>(s.kv[st], &s.kv_full[st], fresh, new_form, box, u.hk, p.B, p.status);
       return true;
     };
-    auto advance = [&](Unit& u) {  // to the next unit with something to load
+    auto advance = [&](TreeUnit& u) {  // to the next unit with something to load
       while (w.next(p, rw, u))
         if (!u.empty) return true;
       return false;
@@ -262,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     TileBox box{};
     if (more) box = find(u, w.s, u.tb);
     while (more) {
-      const Unit v = u;
-      const Seq sq = w.s;
+      const TreeUnit v = u;
+      const TreeSeq sq = w.s;
       const int n = v.te - v.tb;
       for (int t = 0; ok && t <= (v.two ? 1 : 0); ++t, ++nq) {
         const int slot = nq & 1;
@@ -278,25 +256,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      more = advance(u);
       // the order the products consume them in; the next tile's box is looked up
-      // before this one's loads wait for their buffers
+      // between this one's loads
       TileBox prev{};
       for (int i = 0; ok && i <= n; ++i) {
         const TileBox cur = box;
-        if (i + 1 < n)
+        if (i < n && !(ok = load(&tm_k, &tm_kn, v, sq.nc, v.tb + i, cur, seq + seq_k(v.two, i)))) break;
+        if (i + 1 < n) {
           box = find(v, sq, v.tb + i + 1);
-        else if (i + 1 == n && more)
-          box = find(u, w.s, u.tb);
-        if (v.two) {
-          if (i == n) break;
-          if (!(ok = load_tile(&tm_k, &tm_kn, v, sq.nc, v.tb + i, cur, seq + seq_k(true, i)))) break;
-          ok = load_tile(&tm_v, &tm_vn, v, sq.nc, v.tb + i, cur, seq + seq_v(true, i, n));
-        } else {
-          if (i < n && !(ok = load_tile(&tm_k, &tm_kn, v, sq.nc, v.tb + i, cur, seq + seq_k(false, i)))) break;
-          if (i > 0) ok = load_tile(&tm_v, &tm_vn, v, sq.nc, v.tb + i - 1, prev, seq + seq_v(false, i - 1, n));
-          prev = cur;
+        } else if (i + 1 == n) {
+          more = advance(u);
+          if (more) box = find(u, w.s, u.tb);
         }
+        // with two row tiles V follows its K, else the next K
+        const int iv = v.two ? i : i - 1;
+        if (iv >= 0 && iv < n)
+          ok = load(&tm_v, &tm_vn, v, sq.nc, v.tb + iv, v.two ? cur : prev, seq + seq_v(v.two, iv, n));
+        prev = cur;
       }
       if (!ok) break;
       seq += 2 * n;
@@ -334,11 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = (int)(at % NST);
             if (!(ok = mbar_wait(&s.kv_full[st], (at / NST) & 1, ab))) break;
             tc_fence_after();
-            const uint32_t qa = smem_u32(s.q[(nq + (u.two ? m & 1 : 0)) & 1]), ka = smem_u32(s.kv[st]);
+            const uint64_t qd = sdesc_sw128(smem_u32(s.q[(nq + (u.two ? m & 1 : 0)) & 1]), 16, 1024);
+            const uint64_t kd = k_tile_desc<D>(s.kv[st]);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tmem + (m & 1) * 128, sdesc_sw128(qa + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024),
-                     sdesc_sw128(ka + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0);
+              mma_ss(tmem + (m & 1) * 128, sdesc_at(qd, (kk >> 2) * (BM * 128) + (kk & 3) * 32),
+                     k_tile_step(kd, kk), idesc_s, kk > 0);
             mma_commit(&s.s_full[m & 1]);
             if (!u.two || (m & 1)) mma_commit(&s.kv_empty[st]);
             // the last S of a Q tile frees it
@@ -355,11 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = mbar_wait(&s.p_full[str], done[str] & 1, ab))) break;
             ++done[str];
             tc_fence_after();
-            const uint32_t va = smem_u32(s.kv[st]);
+            const uint64_t vd = v_tile_desc<D>(s.kv[st]);
+            const uint32_t accum = !first;
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
-              mma_ts(tmem + 256 + str * D, tmem + str * 128 + kk * 8, sdesc_sw128(va + kk * 2048, KT * 128, 1024),
-                     idesc_pv, !first || kk > 0);
+              mma_ts(tmem + 256 + str * D, tmem + str * 128 + kk * 8, v_tile_step<D>(vd, kk), idesc_pv,
+                     kk > 0 ? 1u : accum);
             if (!u.two || (j & 1)) mma_commit(&s.kv_empty[st]);
             if (j == items - 1) mma_commit(&s.o_done);
           }
@@ -380,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t col_s = tmem + lane_off + str * 128;
     const uint32_t col_o = tmem + lane_off + 256;
-    const float sc2 = p.scale * kLog2e;
+    const uint64_t sc2 = pack_f32x2(p.scale * kLog2e, p.scale * kLog2e);
     const int rows_in_tile = rw.gb * rw.tt;
     uint32_t seq = 0;
     uint32_t seen = 0;  // items of this stream
@@ -404,27 +382,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool cached = tile < nc;
         const int base = (cached ? tile : tile - nc) * KT;
         const int keys = min(KT, (cached ? len : nr) - base);  // keys of this tile that exist
-        if (keys < KT && (!u.two || str == 0)) {
-          // V rows that do not exist take part with P = 0: they have to be finite
-          const uint32_t at = seq + seq_v(u.two, i, n);
-          const int st = (int)(at % NST);
-          ok = __all_sync(0xffffffffu, mbar_wait(&s.kv_full[st], (at / NST) & 1, ab));
-          if (!ok) break;
-          if (r >= keys) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(s.kv[st] + kb * KT * 128 + r * 128 + c * 16) = z;
-          }
-          fence_proxy_async_smem();
-        }
         if (warp_live) {
           tc_fence_after();
           // which keys of an edge tile the row sees: those below hi, of a drafted
           // tree those of its mask words too
           const bool edge = !cached || keys < KT;
-          uint32_t bits[4];
+          uint32_t bits[4] = {0, 0, 0, 0};
           if (edge) {
             const int hi = cached || mrow ? keys : min(keys, t + 1 - base);
 #pragma unroll
@@ -442,63 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          // half a row of scores in base-2 units, hidden ones at -inf
-          uint32_t sr[KT / 2];
-          auto load_half = [&](int half) {
-            tmem_ld32(col_s + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-            tmem_ld32(col_s + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-            tmem_wait_ld();
-            reg_fence(sr);
-#pragma unroll
-            for (int c = 0; c < KT / 2; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * sc2);
-            if (edge) {
-              const uint32_t lo = half ? bits[2] : bits[0], hi = half ? bits[3] : bits[1];
-#pragma unroll
-              for (int c = 0; c < KT / 2; ++c)
-                if (!(((c < 32 ? lo : hi) >> (c & 31)) & 1u)) sr[c] = 0xff800000u;  // -inf
-            }
-          };
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-          auto max_half = [&]() {
-#pragma unroll
-            for (int c = 0; c < KT / 2; c += 2) {
-              mx0 = fmaxf(mx0, __uint_as_float(sr[c]));
-              mx1 = fmaxf(mx1, __uint_as_float(sr[c + 1]));
-            }
-          };
-          // the second half is read twice, which takes half the registers of one
-          // read (128 scores at once spill); P of the first half overwrites only
-          // scores that are in registers
-          load_half(1);
-          max_half();
-          load_half(0);
-          max_half();
-          const float mx = fmaxf(mx0, mx1);
-          const bool move = mx > m + kRescaleThreshold;
-          const float m_next = move ? mx : m;
-          const float alpha = move ? ex2(m - m_next) : 1.f;
-          const float neg_m = m_next == -INFINITY ? 0.f : -m_next;
-          float rs0 = 0.f, rs1 = 0.f;
-          auto store_half = [&](int half) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float p0 = ex2(__uint_as_float(sr[c * 32 + 2 * e]) + neg_m);
-                const float p1 = ex2(__uint_as_float(sr[c * 32 + 2 * e + 1]) + neg_m);
-                rs0 += p0;
-                rs1 += p1;
-                pk[e] = pack_bf16(p0, p1);  // the product's operand; the sum l keeps 32 bits
-              }
-              tmem_st16(col_s + half * 32 + c * 16, pk);
-            }
-          };
-          store_half(0);
-          load_half(1);
-          store_half(1);
-          l = l * alpha + (rs0 + rs1);
-          m = m_next;
+          const SoftmaxStep st = edge ? softmax_tile<true>(col_s, sc2, m, bits) : softmax_tile<false>(col_s, sc2, m, bits);
+          const float alpha = st.alpha;
+          l = l * alpha + st.sum;
+          m = st.m;
           if (it >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -513,6 +423,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
           tc_fence_before();
+        }
+        if (keys < KT && (!u.two || str == 0)) {
+          // V rows that do not exist take part with P = 0: they have to be finite
+          const uint32_t at = seq + seq_v(u.two, i, n);
+          const int st = (int)(at % NST);
+          ok = __all_sync(0xffffffffu, mbar_wait(&s.kv_full[st], (at / NST) & 1, ab));
+          if (!ok) break;
+          if (r >= keys) zero_slot<D>(s.kv[st], r);
+          fence_proxy_async_smem();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.p_full[str]);
@@ -628,16 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The unit that this run ends in the middle of, having held its beginning (u is
   // the run's last unit): its later parts are the next CTAs' first ones.
   if (threadIdx.x == 0) {
-    TreeCut cut{0, 0, 0, 0};
-    if (run.run1 > run.run0 && u.tb == 0 && u.te < u.n)
-      cut = TreeCut{u.b, u.hk, u.pair * 2 + u.two, run_parts(run, u.n - u.te)};
+    TreeCut cut{0, 0, 0, 0, 0};
+    if (!s.abort_flag && run.run1 > run.run0 && u.tb == 0 && u.te < u.n)
+      cut = TreeCut{u.b, u.hk, u.pair, u.two ? 2 : 1, run_parts(runs.total, runs.workers, blockIdx.x, run.run1, u.n - u.te)};
     p.cuts[blockIdx.x] = cut;
   }
 }
 
-// Combine the partials of the units that a cut divides.  Block (c, y): the unit
-// whose first part CTA c holds (second slot) and whose others are the first
-// slots of CTAs c + 1 .. c + more; a warp per row, a lane per D / 32 columns:
+// Combine the partials of the units that a cut divides.  Block (w, y): the unit
+// whose first part worker w holds (second slot) and whose others are the first
+// slots of workers w + 1 .. w + more; a warp per row, a lane per D / 32 columns:
 //   m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i / l.
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
@@ -645,37 +564,49 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeCut cut = p.cuts[blockIdx.x];
   if (cut.more == 0) return;
-  const Rows rw = row_tiles(p.Hq, p.Hkv, p.Nq);
+  const RowTiles& rw = p.rw;
   const int rows = rw.gb * rw.tt, lane = threadIdx.x & 31;
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5), tile = row / rows, r = row % rows;
-  if (tile > (cut.pair2 & 1)) return;
-  const int rt = (cut.pair2 >> 1) * 2 + tile;
+  if (tile >= cut.tiles) return;
+  const int rt = 2 * cut.pair + tile;
   const int t = rt / rw.gblk * rw.tt + r / rw.gb, g = rt % rw.gblk * rw.gb + r % rw.gb;
   if (t >= p.Nq || g >= rw.G) return;
   const float2* ml = reinterpret_cast<const float2*>(p.lse_part);
   auto part_row = [&](int i) {
     return ((long long)((blockIdx.x + i) * 2 + (i == 0)) * p.part_tiles + tile) * rows + r;
   };
-  float m = -INFINITY;
-  for (int i = lane; i <= cut.more; i += 32) m = fmaxf(m, ml[part_row(i)].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f, acc[E];
+  // 32 parts at a time, a lane per part for its (m, l); a part's weight is 0 when
+  // none of its keys is seen (nothing was stored then)
+  float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i <= cut.more; ++i) {
-    const long long at = part_row(i);
-    const float2 x = ml[at];
-    if (x.y == 0.f) continue;  // sees no key of this part; nothing was stored
-    const float w = x.x == -INFINITY ? 1.f : ex2(x.x - m);  // NaN scores: m_i = -inf, l_i = NaN
-    l = fmaf(w, x.y, l);
-    const float* src = p.o_part + at * D + lane * E;
+  for (int i0 = 0; i0 <= cut.more; i0 += 32) {
+    const int n = min(32, cut.more + 1 - i0);
+    const float2 x = lane < n ? ml[part_row(i0 + lane)] : make_float2(-INFINITY, 0.f);
+    float mx = x.x;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 o2 = *reinterpret_cast<const float2*>(src + e);
-      acc[e] = fmaf(w, o2.x, acc[e]);
-      acc[e + 1] = fmaf(w, o2.y, acc[e + 1]);
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float m2 = fmaxf(m, mx), a = m == -INFINITY ? 1.f : ex2(m - m2);
+    // NaN scores: m_i = -inf and l_i = NaN
+    const float w = x.y == 0.f ? 0.f : (x.x == -INFINITY ? 1.f : ex2(x.x - m2));
+    float part = w * x.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    l = fmaf(l, a, part);
+    m = m2;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= a;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* src = p.o_part + part_row(i0 + i) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        float2 o2 = make_float2(0.f, 0.f);
+        if (wi != 0.f) o2 = *reinterpret_cast<const float2*>(src + e);
+        acc[e] = fmaf(wi, o2.x, acc[e]);
+        acc[e + 1] = fmaf(wi, o2.y, acc[e + 1]);
+      }
     }
   }
   const bool none = l == 0.f;
@@ -688,41 +619,21 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     p.lse[((long long)cut.b * p.Hq + cut.hk * rw.G + g) * p.Nq + t] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 template <int D>
-int launch_t(TreeParams p, const Rows& rw, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mkn, mvn;
-  const uint64_t B = p.B, Hq = p.Hq, Hkv = p.Hkv, Nq = p.Nq, S = p.c.page_size;
-  const uint64_t rq = Hq * D * 2, rk = Hkv * D * 2;
-  const uint64_t qd[4] = {D, Hq, Nq, B}, qs[3] = {D * 2, rq, rq * Nq};
-  const uint32_t qb[4] = {64, (uint32_t)rw.gb, (uint32_t)rw.tt, 1};
-  const uint64_t kd[4] = {D, Hkv, S, (uint64_t)p.c.num_pages}, ks[3] = {D * 2, rk, rk * S};
-  const int box = cache_box_rows(p.c);
-  const uint32_t kb[4] = {64, 1, (uint32_t)box, 1};
-  const int nbox = std::min(KT, (p.Nq + 7) / 8 * 8);
-  const uint64_t nd[4] = {D, Hkv, Nq, B}, ns[3] = {D * 2, rk, rk * Nq};
-  const uint32_t nb[4] = {64, 1, (uint32_t)nbox, 1};
-  int rc;
-  if ((rc = encode_tmap_bf16(&mq, p.q, 4, qd, qs, qb))) return rc;
-  if ((rc = encode_tmap_bf16(&mk, p.c.k, 4, kd, ks, kb))) return rc;
-  if ((rc = encode_tmap_bf16(&mv, p.c.v, 4, kd, ks, kb))) return rc;
-  std::memset(&mkn, 0, sizeof(mkn));
-  std::memset(&mvn, 0, sizeof(mvn));
-  if (p.k_new) {
-    if ((rc = encode_tmap_bf16(&mkn, p.k_new, 4, nd, ns, nb))) return rc;
-    if ((rc = encode_tmap_bf16(&mvn, p.v_new, 4, nd, ns, nb))) return rc;
-  }
+int launch_wide(const TreeParams& p, const TreeMaps& m, cudaStream_t st) {
   const size_t smem = sizeof(TreeSmem<D>) + 1024;
   static_assert(sizeof(TreeSmem<D>) + 1024 <= 232448, "shared memory");
   if (cudaFuncSetAttribute(tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  const unsigned ctas = sm_count();
-  tree_kernel<D><<<ctas, kThreads, smem, st>>>(mq, mk, mv, mkn, mvn, p, box, nbox);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  // the merge's launch overlaps the end of the kernel above and waits for it
+  tree_kernel<D><<<sm_count(), kThreads, smem, st>>>(m.q, m.k, m.v, m.k_new, m.v_new, p, m.form, m.new_form);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// The merge's launch overlaps the end of the kernel before it, whose end it waits for.
+template <int D>
+int launch_merge_parts(const TreeParams& p, int workers, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, (unsigned)((rw.gb * rw.tt * p.part_tiles + 7) / 8));
+  cfg.gridDim = dim3((unsigned)workers, (unsigned)((p.rw.gb * p.rw.tt * p.part_tiles + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -730,31 +641,115 @@ int launch_t(TreeParams p, const Rows& rw, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, (const TreeParams)p) != cudaSuccess) return ATTN_ERR_CUDA;
-  count_launch(2);
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int make_maps(const TreeParams& p, TreeMaps& m) {
+  const uint64_t D = p.D, B = p.B, Hq = p.Hq, Nq = p.Nq, rq = Hq * D * 2;
+  const uint64_t qd[4] = {D, Hq, Nq, B}, qs[3] = {D * 2, rq, rq * Nq};
+  const uint32_t qb[4] = {64, (uint32_t)p.rw.gb, (uint32_t)p.rw.tt, 1};
+  int rc;
+  if ((rc = encode_tmap_bf16(&m.q, p.q, 4, qd, qs, qb))) return rc;
+  if ((rc = cache_tile_map(&m.k, &m.form, p.c, p.c.k, p.Hkv, p.D))) return rc;
+  if ((rc = cache_tile_map(&m.v, &m.form, p.c, p.c.v, p.Hkv, p.D))) return rc;
+  std::memset(&m.k_new, 0, sizeof(m.k_new));
+  std::memset(&m.v_new, 0, sizeof(m.v_new));
+  m.new_form = TileForm{8, 0};
+  if (p.k_new) {
+    if ((rc = rows_tile_map(&m.k_new, &m.new_form, p.k_new, p.Hkv, p.D, p.Nq, p.B))) return rc;
+    if ((rc = rows_tile_map(&m.v_new, &m.new_form, p.v_new, p.Hkv, p.D, p.Nq, p.B))) return rc;
+  }
   return ATTN_OK;
+}
+
+RowTiles row_tiles(int Hq, int Hkv, int Nq) {
+  RowTiles r{};
+  r.G = Hq / Hkv;
+  r.gb = std::min(r.G, BM);
+  r.gblk = (r.G + r.gb - 1) / r.gb;
+  const int fit = BM / r.gb;  // tokens that fit a tile
+  int blocks = (Nq + fit - 1) / fit;
+  if (blocks > 1 && r.gblk == 1) blocks = (blocks + 1) / 2 * 2;  // pairs: the same passes over K and V
+  r.tt = (Nq + blocks - 1) / blocks;
+  r.tiles = (Nq + r.tt - 1) / r.tt * r.gblk;
+  return r;
+}
+
+// @@ measured
+constexpr int kFewRows = 16;
+
+// Two slots per worker (the unit its run begins in, the unit it ends in): few rows,
+// two workers per CTA and one row tile; else one worker and one or two.
+struct Layout {
+  RowTiles rw;
+  int workers, part_tiles;
+  size_t rows, o_bytes, ml_bytes, total;
+};
+
+Layout layout(int Hq, int Hkv, int Nq, int D) {
+  auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+  Layout a;
+  a.rw = row_tiles(Hq, Hkv, Nq);
+  const bool few = a.rw.tiles == 1 && a.rw.gb * a.rw.tt <= kFewRows;
+  a.workers = sm_count() * (few ? 2 : 1);
+  a.part_tiles = a.rw.tiles > 1 ? 2 : 1;
+  a.rows = (size_t)a.workers * 2 * a.part_tiles * a.rw.gb * a.rw.tt;
+  a.o_bytes = align256(a.rows * D * 4);
+  a.ml_bytes = align256(a.rows * 8);
+  a.total = a.o_bytes + a.ml_bytes + align256(a.workers * sizeof(TreeCut));
+  return a;
+}
+
+int tile_map(CUtensorMap* map, TileForm* form, const void* base, int Hkv, int D, uint64_t rows, uint64_t pages,
+             int box_rows) {
+  const uint64_t rk = (uint64_t)Hkv * D * 2, KB = D / 64;
+  form->grouped = rows % 8 == 0;
+  form->rows = form->grouped ? box_rows : 8;
+  const uint64_t dims[5] = {64, form->grouped ? 8 : rows, Hkv * KB, form->grouped ? rows / 8 : 1, pages};
+  const uint64_t strides[4] = {rk, 128, form->grouped ? rk * 8 : rk * rows, rk * rows};
+  const uint32_t box[5] = {64, 8, (uint32_t)KB, (uint32_t)form->rows / 8, 1};
+  return encode_tmap_bf16(map, base, 5, dims, strides, box);
 }
 
 }  // namespace
 
-// Two slots per CTA (the unit its run begins in, the unit it ends in) of one or
-// two row tiles, and one cut record per CTA.
-size_t tree_sm100_workspace(int Hq, int Hkv, int Nq, int D) {
-  const Rows rw = row_tiles(Hq, Hkv, Nq);
-  const size_t rows = (size_t)sm_count() * 2 * (rw.tiles > 1 ? 2 : 1) * rw.gb * rw.tt;
-  return align256(rows * D * 4) + align256(rows * 8) + align256((size_t)sm_count() * sizeof(TreeCut));
+// Boxes never straddle a page: the largest power of two that divides it.
+int cache_tile_map(CUtensorMap* map, TileForm* form, const CacheView& c, const void* base, int Hkv, int D) {
+  int box = KT;
+  if (c.table)
+    while (c.page_size % box) box >>= 1;
+  return tile_map(map, form, base, Hkv, D, c.page_size, c.num_pages, box);
 }
 
+// Few rows in all: boxes of a power of two that holds them.
+int rows_tile_map(CUtensorMap* map, TileForm* form, const void* base, int Hkv, int D, int n, int batch) {
+  int box = KT;
+  while (box > 8 && box / 2 >= n) box >>= 1;
+  return tile_map(map, form, base, Hkv, D, n, batch, box);
+}
+
+size_t tree_sm100_workspace(int Hq, int Hkv, int Nq, int D) { return layout(Hq, Hkv, Nq, D).total; }
+
 int launch_tree_sm100(TreeParams p, void* workspace, cudaStream_t st) {
-  const Rows rw = row_tiles(p.Hq, p.Hkv, p.Nq);
-  p.part_tiles = rw.tiles > 1 ? 2 : 1;
+  const Layout a = layout(p.Hq, p.Hkv, p.Nq, p.D);
+  p.rw = a.rw;
+  p.part_tiles = a.part_tiles;
   p.wait_limit = kWaitLimitCycles;
-  const size_t rows = (size_t)sm_count() * 2 * p.part_tiles * rw.gb * rw.tt;
   char* ws = static_cast<char*>(workspace);
   p.o_part = reinterpret_cast<float*>(ws);
-  p.lse_part = reinterpret_cast<float*>(ws + align256(rows * p.D * 4));
-  p.cuts = reinterpret_cast<TreeCut*>(ws + align256(rows * p.D * 4) + align256(rows * 8));
-  return p.D == 64 ? launch_t<64>(p, rw, st) : launch_t<128>(p, rw, st);
+  p.lse_part = reinterpret_cast<float*>(ws + a.o_bytes);
+  p.cuts = reinterpret_cast<TreeCut*>(ws + a.o_bytes + a.ml_bytes);
+  TreeMaps m;
+  int rc = make_maps(p, m);
+  if (rc) return rc;
+  if (a.workers > sm_count())
+    rc = launch_tree_few(p, m, st);
+  else
+    rc = p.D == 64 ? launch_wide<64>(p, m, st) : launch_wide<128>(p, m, st);
+  if (rc) return rc;
+  if ((rc = p.D == 64 ? launch_merge_parts<64>(p, a.workers, st) : launch_merge_parts<128>(p, a.workers, st))) return rc;
+  count_launch(2);
+  return ATTN_OK;
 }
 
 }  // namespace attn

@@ -55,23 +55,21 @@ struct WeightsSmem {
   uint64_t t_full[NT], t_empty[NT];
   uint64_t z_full[NZ], z_empty[NZ], s_full[4], s_empty[4];
   uint64_t half_full, half_empty, drain;
-  RunSmem<kThreads> run;
+  RunSmem<kThreads, 1> run;
   uint32_t tmem_base;
   int abort_flag;
 };
 
 // Row tiles: tt counted rows x gb heads, gblk blocks of heads.
-struct Rows {
-  int G, gb, tt, gblk;
-};
+using Rows = RowTiles;
 
-__host__ __device__ inline Rows row_tiles(int Hq, int Hkv, int max_rows) {
-  Rows r;
+Rows row_tiles(int Hq, int Hkv, int max_rows) {
+  Rows r{};
   r.G = Hq / Hkv;
-  r.gb = r.G < BR ? r.G : BR;
-  const int fit = BR / r.gb;
-  r.tt = fit < max_rows ? fit : max_rows;
+  r.gb = std::min(r.G, BR);
+  r.tt = std::min(BR / r.gb, max_rows);
   r.gblk = (r.G + r.gb - 1) / r.gb;
+  r.tiles = (max_rows + r.tt - 1) / r.tt * r.gblk;
   return r;
 }
 
@@ -253,15 +251,15 @@ ATTN_DEVINL float add_tile(uint32_t col, int width, const float* z, const int* l
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
-                   const WeightsParams p, const int box_rows) {
+                   const WeightsParams p, const TileForm form) {
   using Smem = WeightsSmem<D>;
   constexpr int NT = Smem::NT;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Rows rw = row_tiles(p.Hq, p.Hkv, p.max_rows);
+  const Rows& rw = p.rw;
   const int width = min(BR, (rw.gb * rw.tt + 15) / 16 * 16);  // columns of a row tile
-  const int nk = (long long)p.max_rows * rw.G <= BR ? Smem::kKeysMany : Smem::kKeysFew, nq = NT - nk;
+  const int nk = rw.tiles == 1 ? Smem::kKeysMany : Smem::kKeysFew, nq = NT - nk;
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
     for (int i = 0; i < NT; ++i) {
@@ -294,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_proxy_async_smem();
   tc_fence_before();
-  const Run run = find_run<kThreads>(s.run, p.B, [&](int b) { return load_seq(p, rw, b).per_head * p.Hkv; });
+  find_runs<kThreads, 1>(s.run, p.B, [&](int b) { return load_seq(p, rw, b).per_head * p.Hkv; });
+  const Run& run = s.run.runs.lane[0];
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   const Abort ab{&s.abort_flag, p.status, p.wait_limit};
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpLoad) {
     // ===================================================== K producer
-    auto find = [&](const Unit& u) { return find_box<D>(p.c, u.b, u.kt * KT, w.s.len, box_rows); };
+    auto find = [&](const Unit& u) { return find_box(p.c, form, u.b, u.kt * KT, w.s.len); };
     bool ok = true, more = w.next(p, rw, u);
     TileBox box{};
     if (more) box = find(u);
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((more = w.next(p, rw, u))) box = find(u);
       ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[st], ((i / nk) & 1) ^ 1, ab));
       if (!ok) break;
-      load_cache_tile<D>(s.tile[st], &s.t_full[st], &tm_k, p.c, cur, hk, box_rows, p.status);
+      load_tile<D>(s.tile[st], &s.t_full[st], &tm_k, form, cur, hk, p.c.num_pages, p.status);
     }
     if (s.abort_flag) {
       // leave no copy in flight into shared memory that is about to be released
@@ -434,11 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int buf = step & 3;
           if (!(ok = mbar_wait(&s.s_empty[buf], ((step >> 2) & 1) ^ 1, ab))) break;
           tc_fence_after();
-          const uint32_t ka = smem_u32(s.tile[kst]), qa = smem_u32(s.tile[nk + iq % nq]);
+          const uint64_t kd = k_tile_desc<D>(s.tile[kst]);
+          const uint64_t qd = sdesc_sw128(smem_u32(s.tile[nk + iq % nq]), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + buf * BR, sdesc_sw128(ka + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024),
-                   sdesc_sw128(qa + (kk >> 2) * (BR * 128) + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
+            mma_ss(tmem + buf * BR, k_tile_step(kd, kk),
+                   sdesc_at(qd, (kk >> 2) * (BR * 128) + (kk & 3) * 32), idesc, kk > 0);
           mma_commit(&s.s_full[buf]);
         }
         if (ok) mma_commit(&s.t_empty[kst]);
@@ -531,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the run's last unit): its later parts are the next CTAs' first ones.
   if (threadIdx.x == 0) {
     WeightsCut cut{0, 0, 0, 0};
-    if (run.run1 > run.run0 && u.jb == 0 && u.je < u.n)
-      cut = WeightsCut{u.b, u.hk, u.kt, run_parts(run, u.n - u.je)};
+    if (!s.abort_flag && run.run1 > run.run0 && u.jb == 0 && u.je < u.n)
+      cut = WeightsCut{u.b, u.hk, u.kt, run_parts(s.run.runs.total, s.run.runs.workers, blockIdx.x, run.run1, u.n - u.je)};
     p.cuts[blockIdx.x] = cut;
   }
 }
@@ -584,14 +584,10 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 template <int D>
 int launch_t(const WeightsParams& p, cudaStream_t st) {
   CUtensorMap mk;
-  const uint64_t row = (uint64_t)p.Hkv * D * 2;
-  const uint64_t kd[4] = {D, (uint64_t)p.Hkv, (uint64_t)p.c.page_size, (uint64_t)p.c.num_pages};
-  const uint64_t ks[3] = {D * 2, row, row * p.c.page_size};
-  const int box = cache_box_rows(p.c);
-  const uint32_t kb[4] = {64, 1, (uint32_t)box, 1};
+  TileForm form;
   int rc;
-  if ((rc = encode_tmap_bf16(&mk, p.c.k, 4, kd, ks, kb))) return rc;
-  const Rows rw = row_tiles(p.Hq, p.Hkv, p.max_rows);
+  if ((rc = cache_tile_map(&mk, &form, p.c, p.c.k, p.Hkv, D))) return rc;
+  const Rows& rw = p.rw;
   CUtensorMap mq;
   const uint64_t rq = (uint64_t)p.Hq * D * 2;
   const uint64_t qd[4] = {D, (uint64_t)p.Hq, (uint64_t)p.Nq, (uint64_t)p.B}, qs[3] = {D * 2, rq, rq * p.Nq};
@@ -603,7 +599,7 @@ int launch_t(const WeightsParams& p, cudaStream_t st) {
   if (cudaFuncSetAttribute(weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
   const int ctas = sm_count();
-  weights_kernel<D><<<ctas, kThreads, smem, st>>>(mk, mq, p, box);
+  weights_kernel<D><<<ctas, kThreads, smem, st>>>(mk, mq, p, form);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = p.weights == p.out ? dim3((unsigned)ctas)
@@ -631,6 +627,7 @@ int launch_weights_sm100(WeightsParams p, void* workspace, cudaStream_t st) {
   p.part = static_cast<float*>(workspace);
   p.cuts = reinterpret_cast<WeightsCut*>(static_cast<char*>(workspace) + align256((size_t)sm_count() * 2 * KT * 4));
   p.wait_limit = kWaitLimitCycles;
+  p.rw = row_tiles(p.Hq, p.Hkv, p.max_rows);
   return p.D == 64 ? launch_t<64>(p, st) : launch_t<128>(p, st);
 }
 
