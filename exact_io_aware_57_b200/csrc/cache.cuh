@@ -164,8 +164,9 @@ constexpr int kGroupBytes = D * 16;
 
 // A tensor map of rows [.., h_kv, d] as {64, row, block of a row, group, page}:
 // coordinates (0, row, hk * d / 64, group, page).  Grouped, a row is one of 8 and
-// boxes are `rows` slots; else a row is any, boxes are 8 slots and groups are
-// not used (rows that are no multiple of 8: a group must not pass the last one).
+// boxes are `rows` slots; else a row is any and groups are not used (rows that
+// are no multiple of 8, where a group would pass the last one: boxes of 8; d = 64,
+// where groups lie end to end: boxes of any multiple of 8).
 struct TileForm {
   int rows;  // slots per box
   int grouped;
@@ -183,9 +184,10 @@ ATTN_DEVINL TileBox find_box(const CacheView& c, const TileForm& f, int b, int b
   t.live = min(128 / f.rows, (len - base + f.rows - 1) / f.rows);
   int slot = base + lane * f.rows;
   t.page = b;
-  if (c.table && lane < t.live) {
-    t.page = __ldg(c.table + (long long)b * c.max_pages + slot / c.page_size);
-    slot %= c.page_size;
+  if (c.table) {
+    const int page = slot / c.page_size;
+    t.page = ldg_if(c.table + (long long)b * c.max_pages + page, lane < t.live, 0);
+    slot -= page * c.page_size;
   }
   t.row = f.grouped ? 0 : slot;
   t.group = f.grouped ? slot / 8 : 0;

@@ -116,6 +116,20 @@ ATTN_DEVINL void grouped_unit_at(int i, int nr, int nu, int gs, int& r, int& u) 
 ATTN_DEVINL int linear_block() { return (int)(blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z)); }
 ATTN_DEVINL void grouped_unit(int nr, int nu, int gs, int& r, int& u) { grouped_unit_at(linear_block(), nr, nu, gs, r, u); }
 
+// *p through the read-only path where `on`, else `other`: one predicated load, so
+// that the value is waited for where it is used and not where a branch ends.
+ATTN_DEVINL int ldg_if(const int* p, bool on, int other) {
+  int v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, %3;\n\t@q ld.global.nc.b32 %0, [%1];\n\t}"
+      : "=r"(v)
+      : "l"(p), "r"((int)on), "r"(other));
+  return v;
+}
+ATTN_DEVINL float ldg_if(const float* p, bool on, float other) {
+  return __int_as_float(ldg_if(reinterpret_cast<const int*>(p), on, __float_as_int(other)));
+}
+
 // ------------------------------------------------------------------------- TMA
 ATTN_DEVINL void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

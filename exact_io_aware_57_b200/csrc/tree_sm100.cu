@@ -703,11 +703,13 @@ Layout layout(int Hq, int Hkv, int Nq, int D) {
 int tile_map(CUtensorMap* map, TileForm* form, const void* base, int Hkv, int D, uint64_t rows, uint64_t pages,
              int box_rows) {
   const uint64_t rk = (uint64_t)Hkv * D * 2, KB = D / 64;
-  form->grouped = rows % 8 == 0;
-  form->rows = form->grouped ? box_rows : 8;
+  // with one 64-element block per row groups lie end to end, as rows do
+  form->grouped = KB > 1 && rows % 8 == 0;
+  form->rows = form->grouped || KB == 1 ? box_rows : 8;
   const uint64_t dims[5] = {64, form->grouped ? 8 : rows, Hkv * KB, form->grouped ? rows / 8 : 1, pages};
   const uint64_t strides[4] = {rk, 128, form->grouped ? rk * 8 : rk * rows, rk * rows};
-  const uint32_t box[5] = {64, 8, (uint32_t)KB, (uint32_t)form->rows / 8, 1};
+  const uint32_t box[5] = {64, form->grouped ? 8u : (uint32_t)form->rows, (uint32_t)KB,
+                           form->grouped ? (uint32_t)form->rows / 8 : 1u, 1};
   return encode_tmap_bf16(map, base, 5, dims, strides, box);
 }
 

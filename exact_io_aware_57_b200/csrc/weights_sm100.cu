@@ -16,12 +16,14 @@
 // unit that a cut divides leaves partial sums, added in CTA order by
 // weights_finish_kernel.
 //
-//   warps 0..3   sums of the even steps of the run: thread r owns key r
-//   warps 4..7   sums of the odd steps
-//   warp 8       TMEM owner + single-thread tcgen05.mma issuer
-//   warp 9       TMA producer of K tiles, through the page table
-//   warps 10,11  producers of Q tiles (TMA, or copies by the row list) and of the
-//                rows' -LSE and visible ends
+//   warps 0..15  sums: warpgroup g takes the steps g, g + 4, ... of the run, thread
+//                r key r (with two warpgroups the exponentials' unit stood idle
+//                half the time behind TMEM reads and barriers: an 8192-token
+//                prompt took 485 us instead of @@ us)
+//   warp 16      TMEM owner + single-thread tcgen05.mma issuer
+//   warp 17      TMA producer of K tiles, through the page table
+//   warp 18      producer of Q tiles: TMA, or copies by the row list
+//   warp 19      producer of the rows' -LSE and visible ends
 //
 // TMEM: four score buffers of 128 columns, step s in buffer s & 3.
 #include <algorithm>
@@ -36,8 +38,9 @@ namespace {
 
 constexpr int KT = 128;  // keys per tile (TMEM lanes)
 constexpr int BR = 128;  // rows per tile (columns) at most
-constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpQ = 10;
-constexpr int kThreads = 384;
+constexpr int kSums = 4;  // warpgroups of sums, one per score buffer
+constexpr int kWarpMma = 16, kWarpLoad = 17, kWarpQ = 18, kWarpZ = 19;
+constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr int NZ = 8;  // row-term ring
 
@@ -51,10 +54,10 @@ struct WeightsSmem {
   alignas(1024) uint8_t tile[NT][kTileBytes];
   alignas(16) float z[NZ][BR];  // -LSE log2(e); -inf for a row that counts for nothing
   alignas(16) int last[NZ][BR];  // last slot the row sees
-  float half[KT];  // the odd steps' sums of a unit
+  float part[kSums][KT];  // a unit's sums by the warpgroups that do not finish it
   uint64_t t_full[NT], t_empty[NT];
   uint64_t z_full[NZ], z_empty[NZ], s_full[4], s_empty[4];
-  uint64_t half_full, half_empty, drain;
+  uint64_t part_full, part_empty, drain;
   RunSmem<kThreads, 1> run;
   uint32_t tmem_base;
   int abort_flag;
@@ -123,11 +126,24 @@ ATTN_DEVINL Seq load_seq(const WeightsParams& p, const Rows& rw, int b) {
   return s;
 }
 
+// A place in a ring whose length is known at run time only, kept by counting: a
+// division a step costs the issuing thread as much as its MMAs' issue.
+struct Place {
+  int slot = 0;
+  uint32_t lap = 0;
+  ATTN_DEVINL void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      lap ^= 1;
+    }
+  }
+};
+
 struct Unit {
   int b, hk, kt;
   int first;      // first row tile (of a block of heads)
   int jb, je, n;  // steps [jb, je) of n: row tile first + j / gblk, block of heads j % gblk
-  bool same_q;    // its only row tile is the previous unit's
+  bool same_q;    // launches of one row tile: it is the previous unit's; else each step has its own
 };
 
 struct Walk {
@@ -175,7 +191,7 @@ struct Walk {
     u.n = (s.tiles - u.first) * rw.gblk;
     u.jb = j;
     u.je = (int)min((long long)u.n, j + left);
-    u.same_q = !fresh && s.tiles * rw.gblk == 1;
+    u.same_q = !fresh && rw.tiles == 1;
     left -= u.je - u.jb;
     j = 0;
     ++kt;
@@ -215,32 +231,27 @@ ATTN_DEVINL void add_columns(const uint32_t (&sr)[N], const float* z, const int*
   }
 }
 
-// The same of a whole row tile in TMEM; a full one's next 32 columns are on
-// their way while 32 are summed.
+// The same of a whole row tile in TMEM; a full one's next 16 columns are on
+// their way while 16 are summed.
 template <bool EDGE>
 ATTN_DEVINL float add_tile(uint32_t col, int width, const float* z, const int* last, int key, uint64_t sc) {
   uint64_t a0 = 0, a1 = 0;  // a tile's own sums: short chains round less
+  uint32_t sr[2][16];
+  tmem_ld16(col, sr[0]);
   if (width == BR) {
-    uint32_t sr[2][32];
-    tmem_ld32(col, sr[0]);
-    tmem_wait_ld();
-    reg_fence(sr[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c < 3) tmem_ld32(col + 32 * (c + 1), sr[(c + 1) & 1]);
-      add_columns<EDGE>(sr[c & 1], z + 32 * c, last + 32 * c, key, sc, a0, a1);
-      if (c < 3) {
-        tmem_wait_ld();
-        reg_fence(sr[(c + 1) & 1]);
-      }
+    for (int c = 0; c < BR / 16; ++c) {
+      tmem_wait_ld();
+      reg_fence(sr[c & 1]);
+      if (c + 1 < BR / 16) tmem_ld16(col + 16 * (c + 1), sr[(c + 1) & 1]);
+      add_columns<EDGE>(sr[c & 1], z + 16 * c, last + 16 * c, key, sc, a0, a1);
     }
   } else {
     for (int c = 0; c < width; c += 16) {
-      uint32_t sr[16];
-      tmem_ld16(col + c, sr);
       tmem_wait_ld();
-      reg_fence(sr);
-      add_columns<EDGE>(sr, z + c, last + c, key, sc, a0, a1);
+      reg_fence(sr[0]);
+      add_columns<EDGE>(sr[0], z + c, last + c, key, sc, a0, a1);
+      if (c + 16 < width) tmem_ld16(col + c + 16, sr[0]);
     }
   }
   float x, y;
@@ -268,14 +279,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < NZ; ++i) {
       mbar_init(&s.z_full[i], 1);
-      mbar_init(&s.z_empty[i], 8);
+      mbar_init(&s.z_empty[i], rw.tiles == 1 ? 4 * kSums : 4);  // warps that use a slot (see same_q)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.s_empty[i], 4);
     }
-    mbar_init(&s.half_full, 4);
-    mbar_init(&s.half_empty, 4);
+    mbar_init(&s.part_full, 4 * (kSums - 1));
+    mbar_init(&s.part_empty, 4);
     mbar_init(&s.drain, 1);
     fence_mbar_init();
   }
@@ -307,15 +318,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, more = w.next(p, rw, u);
     TileBox box{};
     if (more) box = find(u);
-    for (int i = 0; more; ++i) {
-      const int st = i % nk, hk = u.hk;
+    for (Place k; more; k.next(nk)) {
+      const int st = k.slot, hk = u.hk;
       const TileBox cur = box;
       // the slots' weights into L2, some tiles before their sums are ready
       const int key = u.kt * KT + lane * 32;
       if (p.weights && lane < 5 && key < w.s.len)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weights + ((long long)u.b * p.Hkv + hk) * p.cap + key));
       if ((more = w.next(p, rw, u))) box = find(u);
-      ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[st], ((i / nk) & 1) ^ 1, ab));
+      ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[st], k.lap ^ 1, ab));
       if (!ok) break;
       load_tile<D>(s.tile[st], &s.t_full[st], &tm_k, form, cur, hk, p.c.num_pages, p.status);
     }
@@ -326,44 +337,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(&s.t_full[st], 1, p.wait_limit / 64);
       }
     }
-  } else if (warp >= kWarpQ) {
-    // ===================================================== Q rows
-    // The two warps take row tiles in turn: -LSE and the last visible slot of
-    // each row, four rows a lane, and the rows themselves.  Rows in their own
-    // order come by TMA; listed rows by 16-byte copies into the same 128-byte
-    // swizzle (chunk c of row r at chunk c ^ (r & 7)).
+  } else if (warp == kWarpQ) {
+    // ===================================================== Q producer
+    // Rows in their own order come by TMA; listed rows by 16-byte copies, a row's
+    // address per lane, into the same 128-byte swizzle (chunk c of row r at chunk
+    // c ^ (r & 7)).
     constexpr int CH = D / 8;  // 16-byte chunks per row
-    int i = 0, issued = 0;     // row tiles passed; loads in flight by this warp
+    Place q;
     bool ok = true;
     while (ok && w.next(p, rw, u)) {
       if (u.same_q) continue;
-      for (int j = u.jb; ok && j < u.je; ++j, ++i) {
-        if ((i & 1) != warp - kWarpQ) continue;
-        const int st = nk + i % nq, zt = i % NZ;
-        const int i0 = (u.first + j / rw.gblk) * rw.tt, g0 = j % rw.gblk * rw.gb;
-        long long src[4];
-        float z[4];
-        int last[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = x * 32 + lane, row = i0 + r / rw.gb, g = g0 + r % rw.gb;
-          src[x] = -1;
-          z[x] = -INFINITY;
-          last[x] = -1;
-          if (r < rw.gb * rw.tt && row < w.s.cnt && g < rw.G) {
-            const int t = p.rows ? __ldg(p.rows + (long long)u.b * p.max_rows + row) : row;
-            if (t < 0 || t >= p.Nq) {
-              atomicExch(p.status, ATTN_ERR_INVALID);
-            } else {
-              const int h = u.hk * rw.G + g;
-              src[x] = (((long long)u.b * p.Nq + t) * p.Hq + h) * D;
-              const float lse = __ldg(p.lse + ((long long)u.b * p.Hq + h) * p.Nq + t);
-              z[x] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-              last[x] = w.s.len - w.s.cnt + row;
-            }
-          }
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[st], ((i / nq) & 1) ^ 1, ab));
+      for (int j = u.jb; j < u.je; ++j, q.next(nq)) {
+        const int st = nk + q.slot, i0 = (u.first + j / rw.gblk) * rw.tt, g0 = j % rw.gblk * rw.gb;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[st], q.lap ^ 1, ab));
         if (!ok) break;
         if (!p.rows) {
           if (lane == 0) {
@@ -373,75 +359,159 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(s.tile[st] + kb * BR * 128, &tm_q, &s.t_full[st], kb * 64, u.hk * rw.G + g0, i0, u.b);
           }
           __syncwarp();
+          continue;
         }
-        issued = 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s.z_empty[zt], ((i / NZ) & 1) ^ 1, ab));
-        if (!ok) break;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          s.z[zt][x * 32 + lane] = z[x];
-          s.last[zt][x * 32 + lane] = last[x];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.z_full[zt]);
-        if (p.rows) {
-          const char* base = static_cast<const char*>(p.q);
-          const uint32_t qs = smem_u32(s.tile[st]);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (x * 32 >= width) break;  // uniform
+        const char* base = static_cast<const char*>(p.q);
+        const uint32_t qs = smem_u32(s.tile[st]);
 #pragma unroll 1
-            for (int y = 0; y < CH; ++y) {
-              const int rr = y * (32 / CH) + lane / CH, c = lane % CH;  // row of the 32, chunk of the row
-              const long long at = __shfl_sync(0xffffffffu, src[x], rr);
-              const int r = x * 32 + rr;
-              const uint32_t dst = qs + (c >> 3) * (BR * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-              // a row that counts for nothing is zeros
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                           "l"(base + (at < 0 ? 0 : at * 2 + c * 16)), "r"(at < 0 ? 0 : 16)
-                           : "memory");
-            }
+        for (int x = 0; x < width; x += 32) {
+          const int row = i0 + (x + lane) / rw.gb, g = g0 + (x + lane) % rw.gb;
+          long long src = -1;
+          if (x + lane < rw.gb * rw.tt && row < w.s.cnt && g < rw.G) {
+            const int t = __ldg(p.rows + (long long)u.b * p.max_rows + row);
+            if (t >= 0 && t < p.Nq) src = (((long long)u.b * p.Nq + t) * p.Hq + u.hk * rw.G + g) * D;
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.t_full[st]);
+#pragma unroll 1
+          for (int y = 0; y < CH; ++y) {
+            const int rr = y * (32 / CH) + lane / CH, c = lane % CH;  // row of the 32, chunk of the row
+            const long long at = __shfl_sync(0xffffffffu, src, rr);
+            const int r = x + rr;
+            const uint32_t dst = qs + (c >> 3) * (BR * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            // a row that counts for nothing is zeros
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                         "l"(base + (at < 0 ? 0 : at * 2 + c * 16)), "r"(at < 0 ? 0 : 16)
+                         : "memory");
+          }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.t_full[st]);
       }
     }
-    if (s.abort_flag && issued && !p.rows) {
+    if (s.abort_flag && !p.rows) {
       for (int st = nk; st < NT; ++st) {
         mbar_wait_drain(&s.t_full[st], 0, p.wait_limit / 64);
         mbar_wait_drain(&s.t_full[st], 1, p.wait_limit / 64);
       }
     }
+  } else if (warp == kWarpZ) {
+    // ===================================================== rows' terms
+    // -LSE and the last visible slot of each row, four rows a lane.
+    int tq[4], gq[4];  // a row's place in a row tile
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = x * 32 + lane;
+      tq[x] = r < rw.gb * rw.tt ? r / rw.gb : 1 << 29;  // (no row)
+      gq[x] = r % rw.gb;
+    }
+    struct Terms {
+      float lse[4];
+      int last[4];
+    };
+    int i = 0, j = 0;  // row tiles stored; step of the unit
+    bool ok = true;
+    u.je = 0;
+    long long base[4];  // lse of the lane's heads in this unit
+    int row[4], len = 0, cnt = 0, gi = 0;  // the lane's rows in this step; block of heads
+    auto place = [&]() {  // rows and heads of the unit's first step here
+      const int i0 = (u.first + j / rw.gblk) * rw.tt;
+      gi = j % rw.gblk;
+      len = w.s.len;
+      cnt = w.s.cnt;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        row[v] = i0 + tq[v];
+        base[v] = ((long long)u.b * p.Hq + u.hk * rw.G + gi * rw.gb + gq[v]) * p.Nq;
+      }
+    };
+    auto advance = [&]() -> bool {  // to the next step that has a row tile of its own
+      if (++j < u.je) {
+        const bool next_rows = ++gi == rw.gblk;
+        if (next_rows) gi = 0;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          row[v] += next_rows ? rw.tt : 0;
+          base[v] += rw.gblk > 1 ? (long long)(next_rows ? 1 - rw.gblk : 1) * rw.gb * p.Nq : 0;
+        }
+        return true;
+      }
+      do {
+        if (!w.next(p, rw, u)) return false;
+      } while (u.same_q);
+      j = u.jb;
+      place();
+      return true;
+    };
+    auto load = [&](Terms& t) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        bool on = row[v] < cnt && gi * rw.gb + gq[v] < rw.G;
+        int k = row[v];
+        if (p.rows) {
+          k = ldg_if(p.rows + (long long)u.b * p.max_rows + row[v], on, 0);
+          if (k < 0 || k >= p.Nq) {
+            atomicExch(p.status, ATTN_ERR_INVALID);
+            on = false;
+          }
+        }
+        t.lse[v] = ldg_if(p.lse + base[v] + k, on, 0.f);
+        t.last[v] = on ? len - cnt + row[v] : -1;
+      }
+    };
+    auto store = [&](const Terms& t) {
+      const int zt = i % NZ;
+      ok = __all_sync(0xffffffffu, mbar_wait(&s.z_empty[zt], ((i / NZ) & 1) ^ 1, ab));
+      if (!ok) return;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        s.z[zt][v * 32 + lane] = t.lse[v] == -INFINITY || t.last[v] < 0 ? -INFINITY : -t.lse[v] * kLog2e;
+        s.last[zt][v * 32 + lane] = t.last[v];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.z_full[zt]);
+      ++i;
+    };
+    // two sets in turn: nothing waits for a load but its own store
+    Terms t0, t1;
+    bool more = advance();
+    if (more) load(t0);
+    while (ok && more) {
+      if ((more = advance())) load(t1);
+      store(t0);
+      if (!ok || !more) break;
+      if ((more = advance())) load(t0);
+      store(t1);
+    }
   } else if (warp == kWarpMma) {
     // ===================================================== MMA issuer
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(KT, width, 0, 0);
-      int i = 0, iq = -1, step = 0;
+      int step = 0;
+      Place k, q;  // the K tile in use; the next Q tile
+      int q_slot = -1;
       bool ok = true;
-      for (; ok && w.next(p, rw, u); ++i) {
-        const int kst = i % nk;
-        if (!(ok = mbar_wait(&s.t_full[kst], (i / nk) & 1, ab))) break;
+      for (; ok && w.next(p, rw, u); k.next(nk)) {
+        if (!(ok = mbar_wait(&s.t_full[k.slot], k.lap, ab))) break;
+        const uint64_t kd = k_tile_desc<D>(s.tile[k.slot]);
         for (int j = u.jb; j < u.je; ++j, ++step) {
           if (!u.same_q) {
-            if (iq >= 0) mma_commit(&s.t_empty[nk + iq % nq]);  // the previous row tile has been used
-            ++iq;
-            if (!(ok = mbar_wait(&s.t_full[nk + iq % nq], (iq / nq) & 1, ab))) break;
+            if (q_slot >= 0) mma_commit(&s.t_empty[q_slot]);  // the previous row tile has been used
+            q_slot = nk + q.slot;
+            if (!(ok = mbar_wait(&s.t_full[q_slot], q.lap, ab))) break;
+            q.next(nq);
           }
           const int buf = step & 3;
           if (!(ok = mbar_wait(&s.s_empty[buf], ((step >> 2) & 1) ^ 1, ab))) break;
           tc_fence_after();
-          const uint64_t kd = k_tile_desc<D>(s.tile[kst]);
-          const uint64_t qd = sdesc_sw128(smem_u32(s.tile[nk + iq % nq]), 16, 1024);
+          const uint64_t qd = sdesc_sw128(smem_u32(s.tile[q_slot]), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + buf * BR, k_tile_step(kd, kk),
-                   sdesc_at(qd, (kk >> 2) * (BR * 128) + (kk & 3) * 32), idesc, kk > 0);
+            mma_ss(tmem + buf * BR, k_tile_step(kd, kk), sdesc_at(qd, (kk >> 2) * (BR * 128) + (kk & 3) * 32), idesc,
+                   kk > 0);
           mma_commit(&s.s_full[buf]);
         }
-        if (ok) mma_commit(&s.t_empty[kst]);
+        if (ok) mma_commit(&s.t_empty[k.slot]);
       }
       // TMEM must be quiescent before it is released
       mma_commit(&s.drain);
@@ -450,62 +520,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ===================================================== sums
     const int wg = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t col = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + wg * BR;
     const uint64_t sc = pack_f32x2(p.scale * kLog2e, p.scale * kLog2e);
+    const bool one = rw.tiles == 1;  // rows' terms shared by all steps of a head, else one step's
     int step = 0, iz = -1, shared = 0;
     bool ok = true;
     while (ok && w.next(p, rw, u)) {
-      const int key = u.kt * KT + r, n = u.je - u.jb;
+      const int key = u.kt * KT + r, n = u.je - u.jb, s0 = step;
       const bool whole = n == u.n;
-      // whose sum is final: of one step its warpgroup's, else the first's
-      const bool owner = n == 1 ? (step & 1) == wg : wg == 0;
+      // who adds up: the warpgroup of the first step here
+      const bool owner = (s0 & 3) == wg;
       const long long at = ((long long)u.b * p.Hkv + u.hk) * p.cap + key;
       float before = 0.f;
       if (owner && whole && key < w.s.len && p.weights) before = p.weights[at];
       float sum = 0.f;
-      for (int j = u.jb; j < u.je; ++j, ++step) {
-        if (!u.same_q) {
-          if (iz >= 0) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.z_empty[iz % NZ]);
-          }
-          ++iz;
-          ok = __all_sync(0xffffffffu, mbar_wait(&s.z_full[iz % NZ], (iz / NZ) & 1, ab));
+      if (one && !u.same_q) {
+        if (iz >= 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.z_empty[iz % NZ]);
+        }
+        ++iz;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.z_full[iz % NZ], (iz / NZ) & 1, ab));
+        if (!ok) break;
+      }
+      // this warpgroup's steps
+      step = s0 + ((wg - s0) & 3);
+      for (; step < s0 + n; step += kSums) {
+        const int zt = one ? iz % NZ : step % NZ, j = u.jb + step - s0;
+        if (!one) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&s.z_full[zt], (step / NZ) & 1, ab));
           if (!ok) break;
         }
-        if ((step & 1) != wg) continue;
-        const int buf = step & 3;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (step >> 2) & 1, ab));
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[wg], (step >> 2) & 1, ab));
         if (!ok) break;
         tc_fence_after();
-        const float* z = s.z[iz % NZ];
-        const int* last = s.last[iz % NZ];
-        const uint32_t col = tmem + lane_off + buf * BR;
+        const float* z = s.z[zt];
+        const int* last = s.last[zt];
         // rows from i0 on: the tile's last key is hidden from the first of them,
         // or the last of them do not count
         const int i0 = (u.first + j / rw.gblk) * rw.tt;
         const bool edge = u.kt * KT + KT - 1 > w.s.len - w.s.cnt + i0 || i0 + rw.tt > w.s.cnt || rw.gblk > 1;
-        const float part = edge ? add_tile<true>(col, width, z, last, key, sc)
-                                : add_tile<false>(col, width, z, last, key, sc);
+        sum += edge ? add_tile<true>(col, width, z, last, key, sc) : add_tile<false>(col, width, z, last, key, sc);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.s_empty[buf]);
-        sum += part;
+        if (lane == 0) {
+          mbar_arrive(&s.s_empty[wg]);
+          if (!one) mbar_arrive(&s.z_empty[zt]);
+        }
       }
       if (!ok) break;
-      if (n > 1) {  // both warpgroups took steps
-        if (wg == 1) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&s.half_empty, (shared & 1) ^ 1, ab));
+      step = s0 + n;
+      if (n > 1) {  // several warpgroups took steps
+        if (owner) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&s.part_full, shared & 1, ab));
           if (!ok) break;
-          s.half[r] = sum;
+          for (int x = 1; x < min(n, kSums); ++x) sum += s.part[(wg + x) & 3][r];
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s.half_full);
+          if (lane == 0) mbar_arrive(&s.part_empty);
         } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(&s.half_full, shared & 1, ab));
+          ok = __all_sync(0xffffffffu, mbar_wait(&s.part_empty, (shared & 1) ^ 1, ab));
           if (!ok) break;
-          sum += s.half[r];
+          s.part[wg][r] = sum;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s.half_empty);
+          if (lane == 0) mbar_arrive(&s.part_full);
         }
         ++shared;
       }
