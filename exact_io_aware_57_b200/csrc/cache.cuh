@@ -164,33 +164,50 @@ constexpr int kGroupBytes = D * 16;
 
 // A tensor map of rows [.., h_kv, d] as {64, row, block of a row, group, page}:
 // coordinates (0, row, hk * d / 64, group, page).  Grouped, a row is one of 8 and
-// boxes are `rows` slots; else a row is any and groups are not used (rows that
+// boxes are any number of slots; else a row is any and groups are not used (rows that
 // are no multiple of 8, where a group would pass the last one: boxes of 8; d = 64,
 // where groups lie end to end: boxes of any multiple of 8).
 struct TileForm {
-  int rows;  // slots per box
+  int shift;  // log2 of the slots per box
   int grouped;
+  int dp, ds;  // 128 slots on: pages, and slots in a page
 };
 
-// Where a lane's box of a tile lies, a lane per box.  Looked up a tile ahead of
-// its load, so that no load waits for the page table.
+// The place of a lane's box (a lane per box) in a sequence, moved on tile by tile:
+// the loading warp's own instructions bound how fast tiles come, and a division by
+// the page size would be a third of them.
+struct TileCursor {
+  int page, slot;
+  ATTN_DEVINL void begin(const CacheView& c, const TileForm& f, int base) {
+    slot = base + ((threadIdx.x & 31) << f.shift);
+    page = c.table ? slot / c.page_size : 0;
+    slot -= page * c.page_size;
+  }
+  ATTN_DEVINL void next(const CacheView& c, const TileForm& f) {
+    page += f.dp;
+    slot += f.ds;
+    if (c.table && slot >= c.page_size) {
+      slot -= c.page_size;
+      ++page;
+    }
+  }
+};
+
+// A lane's box of a tile.  Looked up a tile ahead of its load, so that no load
+// waits for the page table.
 struct TileBox {
   int row, group, page, live;  // live: boxes of the tile that begin below the length
 };
 
-ATTN_DEVINL TileBox find_box(const CacheView& c, const TileForm& f, int b, int base, int len) {
-  const int lane = threadIdx.x & 31;
+// left: slots from the tile's first one to the length.
+ATTN_DEVINL TileBox find_box(const CacheView& c, const TileForm& f, const TileCursor& at, int b, int left) {
   TileBox t;
-  t.live = min(128 / f.rows, (len - base + f.rows - 1) / f.rows);
-  int slot = base + lane * f.rows;
+  t.live = min(128 >> f.shift, (left + (1 << f.shift) - 1) >> f.shift);
   t.page = b;
-  if (c.table) {
-    const int page = slot / c.page_size;
-    t.page = ldg_if(c.table + (long long)b * c.max_pages + page, lane < t.live, 0);
-    slot -= page * c.page_size;
-  }
-  t.row = f.grouped ? 0 : slot;
-  t.group = f.grouped ? slot / 8 : 0;
+  if (c.table)
+    t.page = ldg_if(c.table + (long long)b * c.max_pages + at.page, (int)(threadIdx.x & 31) < t.live, 0);
+  t.row = f.grouped ? 0 : at.slot;
+  t.group = f.grouped ? at.slot >> 3 : 0;
   return t;
 }
 
@@ -200,7 +217,7 @@ template <int D>
 ATTN_DEVINL void load_tile(uint8_t* dst, uint64_t* bar, const CUtensorMap* map, const TileForm& f, const TileBox& t,
                            int hk, int pages, int* status) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0) mbar_expect_tx(bar, t.live * f.rows * D * 2);
+  if (lane == 0) mbar_expect_tx(bar, (t.live << f.shift) * D * 2);
   __syncwarp();
   if (lane < t.live) {
     int page = t.page;
@@ -208,7 +225,7 @@ ATTN_DEVINL void load_tile(uint8_t* dst, uint64_t* bar, const CUtensorMap* map, 
       atomicExch(status, ATTN_ERR_INVALID);
       page = pages;  // outside the tensor: zeros are loaded
     }
-    tma_load_5d(dst + lane * (f.rows / 8) * kGroupBytes<D>, map, bar, 0, t.row, hk * (D / 64), t.group, page);
+    tma_load_5d(dst + (lane << f.shift) * (D * 2), map, bar, 0, t.row, hk * (D / 64), t.group, page);
   }
   __syncwarp();
 }

@@ -87,14 +87,27 @@ struct TreeWalk {
   }
 };
 
-// The box of a unit's tile: of cached slots, or of sequence b's new keys.
-ATTN_DEVINL TileBox tree_box(const TreeParams& p, const TileForm& form, const TileForm& new_form, const TreeSeq& s, int b,
-                             int tile) {
-  if (tile < s.nc) return find_box(p.c, form, b, tile * kTreeKeys, s.len);
-  CacheView rows = p.c;
-  rows.table = nullptr;
-  return find_box(rows, new_form, b, (tile - s.nc) * kTreeKeys, s.nr);
-}
+// A loading warp's place in a unit: boxes of its tiles, of cached slots and then of
+// sequence b's new keys.
+struct TreeBoxes {
+  TileCursor at;
+
+  ATTN_DEVINL TileBox find(const TreeParams& p, const TileForm& form, const TileForm& new_form, const TreeSeq& s, int b,
+                           int tile, bool first) {
+    if (tile < s.nc) {
+      if (first)
+        at.begin(p.c, form, tile * kTreeKeys);
+      else
+        at.next(p.c, form);
+      return find_box(p.c, form, at, b, s.len - tile * kTreeKeys);
+    }
+    CacheView rows = p.c;
+    rows.table = nullptr;
+    TileCursor c;
+    c.begin(rows, new_form, (tile - s.nc) * kTreeKeys);
+    return find_box(rows, new_form, c, b, s.nr - (tile - s.nc) * kTreeKeys);
+  }
+};
 
 template <int N>
 ATTN_DEVINL void reg_fence(uint32_t (&r)[N]) {

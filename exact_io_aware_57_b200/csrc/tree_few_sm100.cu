@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================================================== TMA producer
     Steps it[2];
     TileBox box[2], ahead[2];  // of the step's tile and of the next one, looked up early
+    TreeBoxes boxes[2];
     int nq[2] = {0, 0};        // Q tiles loaded
 #pragma unroll
     for (int l = 0; l < 2; ++l) {
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!x.busy()) return;
       const TreeUnit& u = x.u;
       if (x.first()) {
-        ahead[l] = tree_box(p, form, new_form, x.w.s, u.b, x.tile);
+        ahead[l] = boxes[l].find(p, form, new_form, x.w.s, u.b, x.tile, true);
         const int slot = nq[l] & 1;
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&s.q_empty[l][slot], ((nq[l] >> 1) & 1) ^ 1, ab));
         if (ok && lane == 0) {
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nq[l];
       }
       box[l] = ahead[l];
-      if (x.tile + 1 < u.te) ahead[l] = tree_box(p, form, new_form, x.w.s, u.b, x.tile + 1);
+      if (x.tile + 1 < u.te) ahead[l] = boxes[l].find(p, form, new_form, x.w.s, u.b, x.tile + 1, false);
     };
     // until both runs are over; a lane whose own is passes its positions on
     for (int i = 0; ok; ++i) {

@@ -220,7 +220,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t seq = 0;  // K/V tiles loaded
     int nq = 0;         // Q tiles loaded
     bool ok = true;
-    auto find = [&](const TreeUnit& u, const TreeSeq& q, int tile) { return tree_box(p, form, new_form, q, u.b, tile); };
+    TreeBoxes boxes;
+    auto find = [&](const TreeUnit& u, const TreeSeq& q, int tile) {
+      return boxes.find(p, form, new_form, q, u.b, tile, tile == u.tb);
+    };
     auto load = [&](const CUtensorMap* ctx, const CUtensorMap* fresh, const TreeUnit& u, int nc, int tile,
                     const TileBox& box, uint32_t at) -> bool {
       const int st = (int)(at % NST);
@@ -654,7 +657,7 @@ int make_maps(const TreeParams& p, TreeMaps& m) {
   if ((rc = cache_tile_map(&m.v, &m.form, p.c, p.c.v, p.Hkv, p.D))) return rc;
   std::memset(&m.k_new, 0, sizeof(m.k_new));
   std::memset(&m.v_new, 0, sizeof(m.v_new));
-  m.new_form = TileForm{8, 0};
+  m.new_form = TileForm{};
   if (p.k_new) {
     if ((rc = rows_tile_map(&m.k_new, &m.new_form, p.k_new, p.Hkv, p.D, p.Nq, p.B))) return rc;
     if ((rc = rows_tile_map(&m.v_new, &m.new_form, p.v_new, p.Hkv, p.D, p.Nq, p.B))) return rc;
@@ -705,11 +708,15 @@ int tile_map(CUtensorMap* map, TileForm* form, const void* base, int Hkv, int D,
   const uint64_t rk = (uint64_t)Hkv * D * 2, KB = D / 64;
   // with one 64-element block per row groups lie end to end, as rows do
   form->grouped = KB > 1 && rows % 8 == 0;
-  form->rows = form->grouped || KB == 1 ? box_rows : 8;
+  if (!form->grouped && KB > 1) box_rows = 8;
+  form->shift = 0;
+  while (1 << form->shift < box_rows) ++form->shift;
+  form->dp = 0;
+  form->ds = KT;
   const uint64_t dims[5] = {64, form->grouped ? 8 : rows, Hkv * KB, form->grouped ? rows / 8 : 1, pages};
   const uint64_t strides[4] = {rk, 128, form->grouped ? rk * 8 : rk * rows, rk * rows};
-  const uint32_t box[5] = {64, form->grouped ? 8u : (uint32_t)form->rows, (uint32_t)KB,
-                           form->grouped ? (uint32_t)form->rows / 8 : 1u, 1};
+  const uint32_t box[5] = {64, form->grouped ? 8u : (uint32_t)box_rows, (uint32_t)KB,
+                           form->grouped ? (uint32_t)box_rows / 8 : 1u, 1};
   return encode_tmap_bf16(map, base, 5, dims, strides, box);
 }
 
@@ -720,7 +727,12 @@ int cache_tile_map(CUtensorMap* map, TileForm* form, const CacheView& c, const v
   int box = KT;
   if (c.table)
     while (c.page_size % box) box >>= 1;
-  return tile_map(map, form, base, Hkv, D, c.page_size, c.num_pages, box);
+  const int rc = tile_map(map, form, base, Hkv, D, c.page_size, c.num_pages, box);
+  if (c.table) {
+    form->dp = KT / c.page_size;
+    form->ds = KT % c.page_size;
+  }
+  return rc;
 }
 
 // Few rows in all: boxes of a power of two that holds them.

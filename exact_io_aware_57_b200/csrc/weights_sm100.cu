@@ -147,13 +147,12 @@ struct Unit {
 };
 
 struct Walk {
-  int b, hk, kt, j;
-  long long left;
+  int b, hk, kt, j, left;
   bool any;
   Seq s;
 
   ATTN_DEVINL void begin(const WeightsParams& p, const Rows& rw, const Run& run) {
-    left = run.run1 - run.run0;
+    left = (int)(run.run1 - run.run0);
     any = false;
     if (left <= 0) return;
     b = run.b;
@@ -190,7 +189,7 @@ struct Walk {
     u.first = first_tile(rw, s, kt);
     u.n = (s.tiles - u.first) * rw.gblk;
     u.jb = j;
-    u.je = (int)min((long long)u.n, j + left);
+    u.je = min(u.n, j + left);
     u.same_q = !fresh && rw.tiles == 1;
     left -= u.je - u.jb;
     j = 0;
@@ -314,21 +313,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpLoad) {
     // ===================================================== K producer
-    auto find = [&](const Unit& u) { return find_box(p.c, form, u.b, u.kt * KT, w.s.len); };
+    TileCursor at{0, 0};
+    int b = -1, hk = -1;  // where the cursor is
+    auto find = [&](const Unit& u) {
+      if (u.hk == hk && u.b == b) {
+        at.next(p.c, form);
+      } else {
+        at.begin(p.c, form, u.kt * KT);
+        hk = u.hk;
+        b = u.b;
+      }
+      return find_box(p.c, form, at, u.b, w.s.len - u.kt * KT);
+    };
     bool ok = true, more = w.next(p, rw, u);
     TileBox box{};
     if (more) box = find(u);
     for (Place k; more; k.next(nk)) {
-      const int st = k.slot, hk = u.hk;
       const TileBox cur = box;
-      // the slots' weights into L2, some tiles before their sums are ready
-      const int key = u.kt * KT + lane * 32;
-      if (p.weights && lane < 5 && key < w.s.len)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weights + ((long long)u.b * p.Hkv + hk) * p.cap + key));
+      const int cur_hk = u.hk;
       if ((more = w.next(p, rw, u))) box = find(u);
-      ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[st], k.lap ^ 1, ab));
+      ok = __all_sync(0xffffffffu, mbar_wait(&s.t_empty[k.slot], k.lap ^ 1, ab));
       if (!ok) break;
-      load_tile<D>(s.tile[st], &s.t_full[st], &tm_k, form, cur, hk, p.c.num_pages, p.status);
+      load_tile<D>(s.tile[k.slot], &s.t_full[k.slot], &tm_k, form, cur, cur_hk, p.c.num_pages, p.status);
     }
     if (s.abort_flag) {
       // leave no copy in flight into shared memory that is about to be released
@@ -438,6 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       do {
         if (!w.next(p, rw, u)) return false;
+        // the slots' weights into L2, before their sums are ready
+        const int key = u.kt * KT + lane * 32;
+        if (p.weights && lane < 5 && key < w.s.len)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weights + ((long long)u.b * p.Hkv + u.hk) * p.cap + key));
       } while (u.same_q);
       j = u.jb;
       place();
