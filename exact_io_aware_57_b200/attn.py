@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 from pathlib import Path
 
@@ -405,17 +406,17 @@ class KVCache(ctypes.Structure):
 
 # A decode step makes several of these calls per layer, each of a few
 # microseconds on the device, so their checks are few and cheap: one test per
-# tensor, and the reasons only where it fails.
+# tensor, and the reasons only where it fails.  `dev` is a device index.
 def _ptr(t, name, dtype, shape, dev):
     """Device address of t, a contiguous tensor of this dtype, shape and device."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype:
         raise AttnError(f"{name} must be {dtype}, is {t.dtype}")
     if t.shape != shape:
         raise AttnError(f"{name} must have shape {list(shape)}, has {list(t.shape)}")
-    if t.device != dev:
-        raise AttnError(f"{name} is on {t.device}, not on {dev}")
+    if t.get_device() != dev:
+        raise AttnError(f"{name} is on {t.device}, not on cuda:{dev}")
     raise AttnError(f"{name} must be contiguous")
 
 
@@ -441,34 +442,48 @@ def _row_args(rows, row_lens, B, n, dev):
     return rp, width, None if row_lens is None else _ptr(row_lens, "row_lens", torch.int32, (B,), dev)
 
 
-def _on(t, name):
-    """t's device, and a context in which it is the current one."""
-    dev = t.device
-    if dev.type != "cuda":
-        raise AttnError(f"{name} must be a CUDA tensor")
-    return dev, _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
 _HERE = contextlib.nullcontext()
 
 
+def _on(t, name):
+    """t's device index, and a context in which that device is the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise AttnError(f"{name} must be a CUDA tensor")
+    return dev, _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
 def _dims(t, name, n):
-    if t.dim() != n:
-        raise AttnError(f"{name} must have {n} dimensions, has {list(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != n:
+        raise AttnError(f"{name} must have {n} dimensions, has {list(shape)}")
+    return shape
 
 
 def _stream_on(stream, dev) -> int:
     return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
 
 
-def _scratch(workspace, size, dev):
+def _scratch(workspace, like, dev, size_of, *args):
     """Address and bytes of the caller's workspace, or of a new one (returned to keep it alive)."""
     if workspace is None:
-        workspace = torch.empty(size, device=dev, dtype=torch.uint8)
-    elif workspace.device != dev:
-        raise AttnError(f"workspace is on {workspace.device}, not on {dev}")
+        n = size_of(dev, *args)
+        workspace = like.new_empty(n, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), n
+    if workspace.get_device() != dev:
+        raise AttnError(f"workspace is on {workspace.device}, not on cuda:{dev}")
     return workspace, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+# a size goes by the arguments and the device alone
+@functools.lru_cache(maxsize=4096)
+def _tree_size(dev, *args):
+    return int(_lib.attn_fwd_tree_workspace_size(*args))
+
+
+@functools.lru_cache(maxsize=4096)
+def _weights_size(dev, *args):
+    return int(_lib.attn_cache_weights_workspace_size(*args))
 
 
 def attn_cache_append(k_new, v_new, k_cache, v_cache, cache_lens, block_table=None, rows=None, row_lens=None,
@@ -528,12 +543,12 @@ def attn_fwd_tree(q, k_cache, v_cache, cache_lens, k_new=None, v_new=None, block
         lp = None if row_lens is None else _ptr(row_lens, "row_lens", torch.int32, (B,), dev)
         o = torch.empty_like(q) if out is None else out
         if lse is None:
-            lse = torch.empty((B, Hq, T), device=dev, dtype=torch.float32)
-        size = 0 if workspace is not None else attn_fwd_tree_workspace_size(B, Hq, Hkv, T, d, dt)
-        workspace, wp, wbytes = _scratch(workspace, size, dev)
+            lse = q.new_empty((B, Hq, T), dtype=torch.float32)
+        code = _dtype_code(q)
+        workspace, wp, wbytes = _scratch(workspace, q, dev, _tree_size, B, Hq, Hkv, T, d, code)
         _check(_lib.attn_fwd_tree(_ptr(q, "q", dt, shape, dev), kp, vp, ctypes.byref(c), mp, mstride, lp,
                                   _ptr(o, "out", dt, shape, dev), _ptr(lse, "lse", torch.float32, (B, Hq, T), dev), B,
-                                  Hq, Hkv, T, d, scale, wp, wbytes, _dtype_code(q), _stream_on(stream, dev)))
+                                  Hq, Hkv, T, d, scale, wp, wbytes, code, _stream_on(stream, dev)))
     return o, lse
 
 
@@ -559,15 +574,15 @@ def attn_cache_weights(q, lse, k_cache, cache_lens, weights, block_table=None, r
         if out is None:
             out = weights
             if out is None:
-                out = torch.empty((B, Hkv, c.page_size * c.max_pages), device=dev, dtype=torch.float32)
+                out = q.new_empty((B, Hkv, c.page_size * c.max_pages), dtype=torch.float32)
         cap = out.shape[-1]
         op = _ptr(out, "out", torch.float32, (B, Hkv, cap), dev)
         wp = None if weights is None else _ptr(weights, "weights", torch.float32, (B, Hkv, cap), dev)
-        size = 0 if workspace is not None else attn_cache_weights_workspace_size(B, Hq, Hkv, d, dt)
-        workspace, sp, sbytes = _scratch(workspace, size, dev)
+        code = _dtype_code(q)
+        workspace, sp, sbytes = _scratch(workspace, q, dev, _weights_size, B, Hq, Hkv, d, code)
         _check(_lib.attn_cache_weights(_ptr(q, "q", dt, shape, dev), _ptr(lse, "lse", torch.float32, (B, Hq, T), dev),
                                        ctypes.byref(c), rp, width, lp, wp, op, cap, B, Hq, Hkv, T, d, scale, sp, sbytes,
-                                       _dtype_code(q), _stream_on(stream, dev)))
+                                       code, _stream_on(stream, dev)))
     return out
 
 
@@ -592,7 +607,7 @@ def attn_cache_evict(k_cache, v_cache, weights, cache_lens, keep, k_out, v_out, 
         if weights_out is None:
             weights_out = torch.empty_like(weights)
         if kept is None:
-            kept = torch.empty((B, Hkv, keep), device=dev, dtype=torch.int32)
+            kept = weights.new_empty((B, Hkv, keep), dtype=torch.int32)
         if new_lens is None:
             new_lens = torch.empty_like(cache_lens)
         _check(_lib.attn_cache_evict(ctypes.byref(src), wp, cap, keep, recent, ctypes.byref(dst),
