@@ -39,6 +39,7 @@
 // memory before the product, so rows behind the sequence's end may hold anything.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "tree.cuh"
 
@@ -154,6 +155,28 @@ ATTN_DEVINL SoftmaxStep softmax_tile(uint32_t col_s, uint64_t sc2, float m, cons
   unpack_f32x2(add_f32x2(sum0, sum1), y0, y1);
   r.sum = y0 + y1;
   return r;
+}
+
+// (a call of its own: it is rare, and its registers would be the loop's)
+__device__ __noinline__ SoftmaxStep softmax_edge_tile(uint32_t col_s, uint64_t sc2, float m, uint32_t b0, uint32_t b1,
+                                                      uint32_t b2, uint32_t b3) {
+  const uint32_t bits[4] = {b0, b1, b2, b3};
+  return softmax_tile<true>(col_s, sc2, m, bits);
+}
+
+// O of a row times alpha (likewise).
+template <int D>
+__device__ __noinline__ void rescale_row(uint32_t col_o, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t v[32];
+    tmem_ld32(col_o + c, v);
+    tmem_wait_ld();
+    reg_fence(v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+    tmem_st32(col_o + c, v);
+  }
 }
 
 ATTN_DEVINL void store_bf16_32(__nv_bfloat16* dst, const float (&x)[32]) {
@@ -297,56 +320,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16(BM, KT, 0, 0);  // Q: K-major, K tile: K-major
       constexpr uint32_t idesc_pv = idesc_bf16(BM, D, 0, 1);  // P: TMEM, V tile: MN-major
+      // What the issuing thread does between the MMAs leaves the tensor cores idle,
+      // so the streams are unrolled and little is worked out between them.
       uint32_t seq = 0;
       int nq = 0, units = 0;
-      uint32_t done[2] = {0, 0};  // items of each stream whose P has been taken
+      uint32_t done0 = 0, done1 = 0;  // items of each stream whose P has been taken
       bool ok = true;
       while (ok && w.next(p, rw, u)) {
         if (u.empty) continue;
-        const int n = u.te - u.tb, items = u.two ? 2 * n : n;
-        for (int t = 0; ok && t <= (u.two ? 1 : 0); ++t)
+        const int n = u.te - u.tb, turns = u.two ? n : (n + 1) / 2;
+        const bool two = u.two;
+        const uint64_t q0 = sdesc_sw128(smem_u32(s.q[nq & 1]), 16, 1024);
+        const uint64_t q1 = two ? sdesc_sw128(smem_u32(s.q[(nq + 1) & 1]), 16, 1024) : q0;
+        for (int t = 0; ok && t <= (two ? 1 : 0); ++t)
           ok = mbar_wait(&s.q_full[(nq + t) & 1], ((nq + t) >> 1) & 1, ab);
-        for (int m = 0; ok && m <= items; ++m) {
-          if (m < items) {
-            const int i = u.two ? m >> 1 : m;
-            const uint32_t at = seq + seq_k(u.two, i);
-            const int st = (int)(at % NST);
-            if (!(ok = mbar_wait(&s.kv_full[st], (at / NST) & 1, ab))) break;
-            tc_fence_after();
-            const uint64_t qd = sdesc_sw128(smem_u32(s.q[(nq + (u.two ? m & 1 : 0)) & 1]), 16, 1024);
-            const uint64_t kd = k_tile_desc<D>(s.kv[st]);
+        // S of stream str over key tile i
+        auto scores = [&](auto str_c, int i) {
+          constexpr int str = decltype(str_c)::value;
+          const uint32_t at = seq + seq_k(two, i);
+          const int st = (int)(at % NST);
+          if (!(ok = mbar_wait(&s.kv_full[st], (at / NST) & 1, ab))) return;
+          tc_fence_after();
+          const uint64_t qd = str ? q1 : q0, kd = k_tile_desc<D>(s.kv[st]);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tmem + (m & 1) * 128, sdesc_at(qd, (kk >> 2) * (BM * 128) + (kk & 3) * 32),
-                     k_tile_step(kd, kk), idesc_s, kk > 0);
-            mma_commit(&s.s_full[m & 1]);
-            if (!u.two || (m & 1)) mma_commit(&s.kv_empty[st]);
-            // the last S of a Q tile frees it
-            if (u.two ? m >= items - 2 : m == items - 1) mma_commit(&s.q_empty[(nq + (u.two ? m & 1 : 0)) & 1]);
-          }
-          if (m > 0) {
-            const int j = m - 1, i = u.two ? j >> 1 : j, str = j & 1;
-            const uint32_t at = seq + seq_v(u.two, i, n);
-            const int st = (int)(at % NST);
-            const bool first = j < 2;
-            // the previous unit's O has been read
-            if (j == 0 && units > 0 && !(ok = mbar_wait(&s.o_free, (units - 1) & 1, ab))) break;
-            if (!(ok = mbar_wait(&s.kv_full[st], (at / NST) & 1, ab))) break;
-            if (!(ok = mbar_wait(&s.p_full[str], done[str] & 1, ab))) break;
-            ++done[str];
-            tc_fence_after();
-            const uint64_t vd = v_tile_desc<D>(s.kv[st]);
-            const uint32_t accum = !first;
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + str * 128, sdesc_at(qd, (kk >> 2) * (BM * 128) + (kk & 3) * 32), k_tile_step(kd, kk), idesc_s,
+                   kk > 0);
+          mma_commit(&s.s_full[str]);
+          if (!two || str == 1) mma_commit(&s.kv_empty[st]);
+          if (i == n - 1) mma_commit(&s.q_empty[(nq + (two ? str : 0)) & 1]);  // the last S of a Q tile frees it
+        };
+        // O of stream str += P V_i; first: its first of the unit
+        auto product = [&](auto str_c, int i, bool first) {
+          constexpr int str = decltype(str_c)::value;
+          if (!ok) return;
+          // the previous unit's O has been read
+          if (str == 0 && first && units > 0 && !(ok = mbar_wait(&s.o_free, (units - 1) & 1, ab))) return;
+          const uint32_t at = seq + seq_v(two, i, n);
+          const int st = (int)(at % NST);
+          uint32_t& done = str ? done1 : done0;
+          // (V first: it is there as a rule, and is looked at while P is not)
+          if (!(ok = mbar_wait(&s.kv_full[st], (at / NST) & 1, ab))) return;
+          if (!(ok = mbar_wait(&s.p_full[str], done & 1, ab))) return;
+          ++done;
+          tc_fence_after();
+          const uint64_t vd = v_tile_desc<D>(s.kv[st]);
+          const uint32_t accum = !first;
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              mma_ts(tmem + 256 + str * D, tmem + str * 128 + kk * 8, v_tile_step<D>(vd, kk), idesc_pv,
-                     kk > 0 ? 1u : accum);
-            if (!u.two || (j & 1)) mma_commit(&s.kv_empty[st]);
-            if (j == items - 1) mma_commit(&s.o_done);
-          }
+          for (int kk = 0; kk < KT / 16; ++kk)
+            mma_ts(tmem + 256 + str * D, tmem + str * 128 + kk * 8, v_tile_step<D>(vd, kk), idesc_pv, kk > 0 ? 1u : accum);
+          if (!two || str == 1) mma_commit(&s.kv_empty[st]);
+        };
+        const std::integral_constant<int, 0> s0;
+        const std::integral_constant<int, 1> s1;
+        for (int k = 0; ok && k < turns; ++k) {
+          scores(s0, two ? k : 2 * k);
+          if (k > 0) product(s1, two ? k - 1 : 2 * k - 1, k == 1);
+          if (ok && (two || 2 * k + 1 < n)) scores(s1, two ? k : 2 * k + 1);
+          product(s0, two ? k : 2 * k, k == 0);
         }
+        if (two || n % 2 == 0) product(s1, n - 1, turns == 1);
+        if (!ok) break;
+        mma_commit(&s.o_done);
         seq += 2 * n;
-        nq += u.two ? 2 : 1;
+        nq += two ? 2 : 1;
         ++units;
       }
       // TMEM must be quiescent before it is released
@@ -408,27 +445,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const SoftmaxStep st = edge ? softmax_tile<true>(col_s, sc2, m, bits) : softmax_tile<false>(col_s, sc2, m, bits);
+          const SoftmaxStep st = edge ? softmax_edge_tile(col_s, sc2, m, bits[0], bits[1], bits[2], bits[3])
+                                      : softmax_tile<false>(col_s, sc2, m, bits);
           const float alpha = st.alpha;
           l = l * alpha + st.sum;
           m = st.m;
           if (it >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t orr[32];
-              tmem_ld32(col_o + str * D + c * 32, orr);
-              tmem_wait_ld();
-              reg_fence(orr);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-              tmem_st32(col_o + str * D + c * 32, orr);
-            }
+            rescale_row<D>(col_o + str * D, alpha);
           }
           tmem_wait_st();
           tc_fence_before();
         }
         if (keys < KT && (!u.two || str == 0)) {
           // V rows that do not exist take part with P = 0: they have to be finite
+          // (of two row tiles the first one's product comes first)
           const uint32_t at = seq + seq_v(u.two, i, n);
           const int st = (int)(at % NST);
           ok = __all_sync(0xffffffffu, mbar_wait(&s.kv_full[st], (at / NST) & 1, ab));
