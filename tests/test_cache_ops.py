@@ -85,6 +85,16 @@ def test_tree(lens, Hq, Hkv, d, page, T, shape, row_lens, dtype):
     run_tree(Cache(lens, Hkv, d, page, dtype), Hq, T, shape, dtype, row_lens)
 
 
+@pytest.mark.parametrize("T,shape,d,page", [(1, "chain", 128, 16), (7, "tree", 64, 8), (40, "tree", 128, 0),
+                                            (50, "chain", 64, 32), (64, "tree", 128, 128)])
+def test_tree_at_every_place_of_a_tile(T, shape, d, page):
+    """New keys behind 1 .. 128 slots of a tile: sharing it or in a tile of their own."""
+    lens = [1, 7, 8, 9, 31, 33, 63, 64, 65, 77, 88, 95, 119, 120, 121, 127, 128]
+    rng = np.random.default_rng(T)
+    run_tree(Cache([n + 128 * int(k) for n, k in zip(lens, rng.integers(0, 3, len(lens)))], 1, d, page, BF), 2, T, shape,
+             BF, [int(x) for x in rng.integers(0, T + 1, len(lens))])
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_tree_rows_without_any_key(dtype):
     """A mask that leaves a row empty, over an empty and over a used cache."""
