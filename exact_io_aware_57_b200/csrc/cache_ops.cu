@@ -29,7 +29,9 @@ namespace cg = cooperative_groups;
 constexpr int kCopyThreads = 256;
 
 // ------------------------------------------------------------------- append
-__global__ void __launch_bounds__(kCopyThreads) append_kernel(AppendParams p) {
+// `lanes` threads (a power of two, a warp at most) share a row, so that one of them
+// has up to four chunks of K and of V on their way at once.
+__global__ void __launch_bounds__(kCopyThreads) append_kernel(AppendParams p, int lanes) {
   const int b = blockIdx.y;
   int len, n;
   bool ok = cache_len(p.c, b, 1ll << 31, p.status, len) && row_count(p.row_lens, b, p.max_rows, p.status, n);
@@ -38,24 +40,38 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(AppendParams p) {
     ok = false;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) p.new_lens[b] = ok ? len + n : p.c.lens[b];
-  if (!ok) return;
-  const int chunks = p.row_bytes / 16;
-  const long long total = (long long)n * chunks;
-  for (long long i = (long long)blockIdx.x * kCopyThreads + threadIdx.x; i < total;
-       i += (long long)gridDim.x * kCopyThreads) {
-    const int row = (int)(i / chunks), c = (int)(i % chunks);
-    const int t = p.rows ? __ldg(p.rows + (long long)b * p.max_rows + row) : row;
-    if (t < 0 || t >= p.n_new) {
-      atomicExch(p.status, ATTN_ERR_INVALID);
-      continue;
+  const int per = kCopyThreads / lanes, first = threadIdx.x % lanes, chunks = p.row_bytes / 16;
+  const long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;
+  if (!ok || row >= n) return;
+  const int t = p.rows ? __ldg(p.rows + (long long)b * p.max_rows + row) : (int)row;
+  if (t < 0 || t >= p.n_new) {
+    atomicExch(p.status, ATTN_ERR_INVALID);
+    return;
+  }
+  const long long to = cache_row(p.c, b, len + (int)row, p.status);
+  if (to < 0) return;
+  const uint4* k = static_cast<const uint4*>(p.k_new) + ((long long)b * p.n_new + t) * chunks;
+  const uint4* v = static_cast<const uint4*>(p.v_new) + ((long long)b * p.n_new + t) * chunks;
+  uint4* k_to = static_cast<uint4*>(p.c.k) + to * chunks;
+  uint4* v_to = static_cast<uint4*>(p.c.v) + to * chunks;
+  int c = first;
+  for (; c + 3 * lanes < chunks; c += 4 * lanes) {
+    uint4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __ldg(k + c + i * lanes);
+      y[i] = __ldg(v + c + i * lanes);
     }
-    const long long to = cache_row(p.c, b, len + row, p.status);
-    if (to < 0) continue;
-    const long long src = ((long long)b * p.n_new + t) * chunks + c, dst = to * chunks + c;
-    const uint4 kk = __ldg(static_cast<const uint4*>(p.k_new) + src);
-    const uint4 vv = __ldg(static_cast<const uint4*>(p.v_new) + src);
-    static_cast<uint4*>(p.c.k)[dst] = kk;
-    static_cast<uint4*>(p.c.v)[dst] = vv;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      k_to[c + i * lanes] = x[i];
+      v_to[c + i * lanes] = y[i];
+    }
+  }
+  for (; c < chunks; c += lanes) {
+    const uint4 x = __ldg(k + c), y = __ldg(v + c);
+    k_to[c] = x;
+    v_to[c] = y;
   }
 }
 
@@ -275,17 +291,20 @@ __global__ void __launch_bounds__(kCopyThreads) gather_kernel(EvictParams p) {
 }  // namespace
 
 int launch_append(const AppendParams& p, cudaStream_t st) {
-  const long long chunks = (long long)p.max_rows * (p.row_bytes / 16);
-  const dim3 grid((unsigned)std::max(1ll, std::min((chunks + kCopyThreads - 1) / kCopyThreads, 1ll << 20)), (unsigned)p.B);
-  append_kernel<<<grid, kCopyThreads, 0, st>>>(p);
+  int lanes = 32;
+  while (lanes > 1 && lanes / 2 >= p.row_bytes / 16) lanes /= 2;
+  const int per = kCopyThreads / lanes;
+  append_kernel<<<dim3((unsigned)((p.max_rows + per - 1) / per), (unsigned)p.B), kCopyThreads, 0, st>>>(p, lanes);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 int launch_evict(const EvictParams& p, cudaStream_t st) {
-  // CTAs per (sequence, head): shares of about 2048 weights, eight at most
+  // CTAs per (sequence, head): shares of about 2048 weights, eight at most, and no
+  // more than run at one time (three per SM)
+  const long long units = (long long)p.B * p.Hkv;
   int nc = 1;
-  while (nc < 8 && (long long)nc * 2048 < p.cap) nc *= 2;
+  while (nc < 8 && (long long)nc * 2048 < p.cap && 2 * nc * units <= 3ll * sm_count()) nc *= 2;
   cudaLaunchAttribute attr[2]{};
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = nc;
