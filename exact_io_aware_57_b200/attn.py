@@ -464,6 +464,13 @@ def _stream_on(stream, dev) -> int:
     return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
 
 
+def _used_on(stream, *tensors):
+    """Tensors made for a call on a stream that is not the current one outlive it there."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _scratch(workspace, like, dev, size_of, *args):
     """Address and bytes of the caller's workspace, or of a new one (returned to keep it alive)."""
     if workspace is None:
@@ -501,6 +508,7 @@ def attn_cache_append(k_new, v_new, k_cache, v_cache, cache_lens, block_table=No
         rp, width, lp = _row_args(rows, row_lens, B, T, dev)
         if new_lens is None:
             new_lens = torch.empty_like(cache_lens)
+            _used_on(stream, new_lens)
         _check(_lib.attn_cache_append(_ptr(k_new, "k_new", dt, shape, dev), _ptr(v_new, "v_new", dt, shape, dev),
                                       ctypes.byref(c), rp, width, lp,
                                       _ptr(new_lens, "new_lens", torch.int32, (B,), dev), B, T, Hkv, d,
@@ -546,6 +554,7 @@ def attn_fwd_tree(q, k_cache, v_cache, cache_lens, k_new=None, v_new=None, block
             lse = q.new_empty((B, Hq, T), dtype=torch.float32)
         code = _dtype_code(q)
         workspace, wp, wbytes = _scratch(workspace, q, dev, _tree_size, B, Hq, Hkv, T, d, code)
+        _used_on(stream, o, lse, workspace)
         _check(_lib.attn_fwd_tree(_ptr(q, "q", dt, shape, dev), kp, vp, ctypes.byref(c), mp, mstride, lp,
                                   _ptr(o, "out", dt, shape, dev), _ptr(lse, "lse", torch.float32, (B, Hq, T), dev), B,
                                   Hq, Hkv, T, d, scale, wp, wbytes, code, _stream_on(stream, dev)))
@@ -580,6 +589,7 @@ def attn_cache_weights(q, lse, k_cache, cache_lens, weights, block_table=None, r
         wp = None if weights is None else _ptr(weights, "weights", torch.float32, (B, Hkv, cap), dev)
         code = _dtype_code(q)
         workspace, sp, sbytes = _scratch(workspace, q, dev, _weights_size, B, Hq, Hkv, d, code)
+        _used_on(stream, out, workspace)
         _check(_lib.attn_cache_weights(_ptr(q, "q", dt, shape, dev), _ptr(lse, "lse", torch.float32, (B, Hq, T), dev),
                                        ctypes.byref(c), rp, width, lp, wp, op, cap, B, Hq, Hkv, T, d, scale, sp, sbytes,
                                        code, _stream_on(stream, dev)))
@@ -610,6 +620,7 @@ def attn_cache_evict(k_cache, v_cache, weights, cache_lens, keep, k_out, v_out, 
             kept = weights.new_empty((B, Hkv, keep), dtype=torch.int32)
         if new_lens is None:
             new_lens = torch.empty_like(cache_lens)
+        _used_on(stream, weights_out, kept, new_lens)
         _check(_lib.attn_cache_evict(ctypes.byref(src), wp, cap, keep, recent, ctypes.byref(dst),
                                      _ptr(weights_out, "weights_out", torch.float32, wshape, dev),
                                      _ptr(kept, "kept", torch.int32, (B, Hkv, keep), dev),

@@ -15,13 +15,17 @@ struct CacheView {
   int num_pages, page_size, max_pages;  // max_pages 1 without a table
 };
 
-ATTN_DEVINL long long cache_capacity(const CacheView& c) { return (long long)c.max_pages * c.page_size; }
+constexpr int kMaxSlots = 1 << 28;  // per sequence
+
+ATTN_DEVINL long long cache_capacity(const CacheView& c) {
+  return min((long long)kMaxSlots, (long long)c.max_pages * c.page_size);
+}
 
 // Slots of sequence b in use; false (and ATTN_ERR_INVALID in the status word)
 // for a length that is negative or beyond `most` slots.
-ATTN_DEVINL bool cache_len(const CacheView& c, int b, long long most, int* status, int& len) {
+ATTN_DEVINL bool cache_len(const CacheView& c, int b, int most, int* status, int& len) {
   len = c.lens[b];
-  if (len < 0 || len > min(most, cache_capacity(c))) {
+  if (len < 0 || len > min((long long)most, cache_capacity(c))) {
     atomicExch(status, ATTN_ERR_INVALID);
     return false;
   }

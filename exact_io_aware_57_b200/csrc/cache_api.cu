@@ -9,7 +9,8 @@ using namespace attn;
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -28,6 +29,7 @@ int check_sizes(int batch, int h_q, int h_kv, int d, int dtype) {
 int check_cache(const attn_kv_cache* c, int batch, bool need_v, bool need_lens, CacheView& v) {
   if (!c || !c->k || (need_v && !c->v) || (need_lens && !c->lens)) return ATTN_ERR_INVALID;
   if (!aligned16(c->k) || !aligned16(c->v)) return ATTN_ERR_INVALID;
+  if (!aligned(c->block_table, 4) || !aligned(c->lens, 4)) return ATTN_ERR_INVALID;
   if (c->num_pages <= 0 || c->page_size <= 0) return ATTN_ERR_INVALID;
   if (c->block_table) {
     if (c->max_pages <= 0 || c->page_size % 8 != 0) return ATTN_ERR_INVALID;
@@ -69,7 +71,8 @@ int attn_cache_append(const void* k_new, const void* v_new, const attn_kv_cache*
   if ((rc = check_cache(cache, batch, true, true, p.c))) return rc;
   if (!k_new || !v_new || !new_lens || new_lens == cache->lens || n_new <= 0 || max_rows <= 0) return ATTN_ERR_INVALID;
   if (!rows && max_rows > n_new) return ATTN_ERR_INVALID;
-  if (!aligned16(k_new) || !aligned16(v_new)) return ATTN_ERR_INVALID;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned(rows, 4) || !aligned(row_lens, 4) || !aligned(new_lens, 4))
+    return ATTN_ERR_INVALID;
   if (n_new > kMaxSeqLen || max_rows > kMaxSeqLen) return ATTN_ERR_UNSUPPORTED;
   if (!supported_device()) return ATTN_ERR_UNSUPPORTED;
   p.k_new = k_new;
@@ -106,6 +109,7 @@ int attn_fwd_tree(const void* q, const void* k_new, const void* v_new, const att
   if (tree_mask && (!k_new || (mask_batch_stride != 0 && mask_batch_stride < (long long)n_q * p.mask_words)))
     return ATTN_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(o)) return ATTN_ERR_INVALID;
+  if (!aligned(tree_mask, 8) || !aligned(row_lens, 4) || !aligned(lse, 4)) return ATTN_ERR_INVALID;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_WORKSPACE;
   if (!supported_device()) return ATTN_ERR_UNSUPPORTED;
   p.q = q;
@@ -149,7 +153,9 @@ int attn_cache_weights(const void* q, const float* lse, const attn_kv_cache* cac
   if ((rc = check_cache(cache, batch, false, true, p.c))) return rc;
   if (!q || !lse || !out || n_q <= 0 || max_rows <= 0 || cap <= 0) return ATTN_ERR_INVALID;
   if (!rows && max_rows > n_q) return ATTN_ERR_INVALID;
-  if (!aligned16(q)) return ATTN_ERR_INVALID;
+  if (!aligned16(q) || !aligned(lse, 4) || !aligned(rows, 4) || !aligned(row_lens, 4) || !aligned(weights, 4) ||
+      !aligned(out, 4))
+    return ATTN_ERR_INVALID;
   if (n_q > kMaxSeqLen || max_rows > kMaxSeqLen || cap > kMaxSeqLen) return ATTN_ERR_UNSUPPORTED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       workspace_bytes < attn_cache_weights_workspace_size(batch, h_q, h_kv, d, dtype))
@@ -184,6 +190,7 @@ int attn_cache_evict(const attn_kv_cache* cache, const float* weights, int cap, 
   if ((rc = check_cache(dst, batch, true, false, p.dst))) return rc;
   if (!weights || !weights_out || weights == weights_out || !kept || !new_lens || new_lens == cache->lens)
     return ATTN_ERR_INVALID;
+  if (!aligned(weights, 4) || !aligned(weights_out, 4) || !aligned(kept, 4) || !aligned(new_lens, 4)) return ATTN_ERR_INVALID;
   if (cap <= 0 || keep <= 0 || recent < 0 || recent > keep) return ATTN_ERR_INVALID;
   // rows move in no order: the source has to stay as it is
   if (cache->k == dst->k || cache->v == dst->v || cache->k == dst->v || cache->v == dst->k) return ATTN_ERR_INVALID;

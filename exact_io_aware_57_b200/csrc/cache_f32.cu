@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(32 * ROWS) tree_f32_kernel(TreeParams p) {
   const int r = blockIdx.x * ROWS + warp;  // row (t, g) of the group
   const int t = r / G, h = hk * G + r % G;
   int len, nr;
-  if (!cache_len(p.c, b, 1ll << 31, p.status, len) || !row_count(p.row_lens, b, p.Nq, p.status, nr)) len = nr = 0;
+  if (!cache_len(p.c, b, kMaxSlots, p.status, len) || !row_count(p.row_lens, b, p.Nq, p.status, nr)) len = nr = 0;
   const bool valid = t < p.Nq;
   const bool row_ok = t < nr;
   const int n_new = p.k_new ? nr : 0;

@@ -34,7 +34,7 @@ constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads) append_kernel(AppendParams p, int lanes) {
   const int b = blockIdx.y;
   int len, n;
-  bool ok = cache_len(p.c, b, 1ll << 31, p.status, len) && row_count(p.row_lens, b, p.max_rows, p.status, n);
+  bool ok = cache_len(p.c, b, kMaxSlots, p.status, len) && row_count(p.row_lens, b, p.max_rows, p.status, n);
   if (ok && len + (long long)n > cache_capacity(p.c)) {
     atomicExch(p.status, ATTN_ERR_INVALID);
     ok = false;

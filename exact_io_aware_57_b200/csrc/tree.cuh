@@ -24,7 +24,7 @@ struct TreeSeq {
 
 ATTN_DEVINL TreeSeq tree_seq(const TreeParams& p, const RowTiles& rw, int b) {
   TreeSeq s;
-  if (!cache_len(p.c, b, 1ll << 31, p.status, s.len) || !row_count(p.row_lens, b, p.Nq, p.status, s.nr))
+  if (!cache_len(p.c, b, kMaxSlots, p.status, s.len) || !row_count(p.row_lens, b, p.Nq, p.status, s.nr))
     s.len = s.nr = 0;
   s.nc = (s.len + kTreeKeys - 1) / kTreeKeys;
   s.n = s.nc + (p.k_new ? (s.nr + kTreeKeys - 1) / kTreeKeys : 0);

@@ -350,9 +350,10 @@ int attn_cache_append(const void* k_new, const void* v_new, const attn_kv_cache*
  * do all rows of a sequence whose length or count is not acceptable.
  * The value rows of cached slots and of new keys j < row_lens[b] take part in
  * matrix products with P = 0 where a row does not see them: they must be finite.
- * n_q <= 4096.  workspace: DEVICE, 256-byte aligned,
- * attn_fwd_tree_workspace_size(...) bytes, contents need not be initialised;
- * calls that may overlap on the device need one each.
+ * n_q <= 4096; tree_mask 8-byte aligned.  workspace: DEVICE, 256-byte aligned,
+ * attn_fwd_tree_workspace_size(...) bytes for the current device (bf16: 40 MB at
+ * most, whatever the batch and the lengths), contents need not be initialised;
+ * calls that may overlap on the device, in graphs too, need one each.
  */
 size_t attn_fwd_tree_workspace_size(int batch, int h_q, int h_kv, int n_q, int d, int dtype);
 int attn_fwd_tree(const void* q, const void* k_new, const void* v_new, const attn_kv_cache* cache,

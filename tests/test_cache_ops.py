@@ -111,6 +111,18 @@ def test_tree_scales(scale, sigma):
     run_tree(Cache([333, 1200], 2, 128, 64, BF), 8, 9, "tree", BF, scale=scale, sigma=sigma)
 
 
+@pytest.mark.parametrize("T,Hq", [(1, 4), (3, 8), (40, 8)])
+def test_tree_scores_that_rise_and_fall(T, Hq):
+    """Scores hundreds apart, larger from tile to tile in one sequence and smaller in the
+    other: references are raised on the way, and first ones stay the largest."""
+    cache = Cache([900, 900], 2, 128, 16, BF)
+    for b, ramp in enumerate((torch.linspace(0, 60, 900), torch.linspace(60, 0, 900))):
+        cache.rows_k[b] = (cache.rows_k[b].float() * ramp[:, None, None]).to(BF)
+        for i in range(900):
+            cache.k[cache.at(b, i)] = cache.rows_k[b][i]
+    run_tree(cache, Hq, T, "chain", BF)
+
+
 def test_tree_infinite_stale_rows():
     run_tree(Cache([100, 250], 2, 128, 32, BF, stale=math.inf), 8, 4, "chain", BF)
 
@@ -120,6 +132,13 @@ def test_tree_many_and_few_units(B, Hkv):
     """Sequences of very different lengths shared out over the SMs."""
     rng = np.random.default_rng(B)
     run_tree(Cache([int(x) for x in rng.integers(0, 900, B)], Hkv, 64, 16, BF), 2 * Hkv, 3, "tree", BF)
+
+
+@pytest.mark.parametrize("T,Hq", [(1, 2), (5, 16)])
+def test_tree_more_sequences_than_threads(T, Hq):
+    rng = np.random.default_rng(9)
+    run_tree(Cache([int(x) for x in rng.integers(0, 40, 700)], 1, 64, 8, BF), Hq, T, "chain", BF,
+             [int(x) for x in rng.integers(0, T + 1, 700)])
 
 
 def test_tree_long_context():
@@ -152,6 +171,8 @@ WEIGHTS = [
     ([65, 0, 3], 4, 2, 128, 24, 9, [9, 0, 3], 20, False, BF),
     ([4], 160, 1, 128, 0, 4, None, 0, False, BF),
     ([3, 40], 4, 2, 64, 8, 8, [8, 8], 1, False, BF),           # more rows than slots: the first see nothing
+    ([5 + i % 31 for i in range(700)], 2, 1, 64, 8, 1, None, 2, False, BF),   # more sequences than threads
+    ([1500], 24, 2, 128, 0, 1500, None, 0, False, BF),         # 12 heads: row tiles of 120 rows
     ([300], 2, 1, 128, 0, 300, None, 0, False, F32),
     ([129, 64], 8, 4, 64, 16, 6, [6, 2], 5, True, F32),
 ]
@@ -253,17 +274,17 @@ EVICT = [
     ([300, 70], 1, 128, 64, 0, 64, 64, F32),     # only the recent ones stay
     ([33, 34], 8, 64, 8, 8, 33, 1, F32),
     ([20000], 1, 64, 256, 256, 1, 0, BF),
-    ([70000], 2, 64, 0, 0, 30000, 5, BF),
 ]
+# long ones: a share of the weights for each CTA, and shares beyond shared memory
+EVICT_LONG = [([70000], 2, 64, 0, 0, 30000, 5, BF), ([120000], 1, 64, 128, 256, 50000, 0, BF)]
 
 
-@pytest.mark.parametrize("values", ["random", "ties", "equal", "special"])
-@pytest.mark.parametrize("lens,Hkv,d,page,page_out,keep,recent,dtype", EVICT)
+@pytest.mark.parametrize("lens,Hkv,d,page,page_out,keep,recent,dtype,values",
+                         [(*c, v) for c in EVICT for v in ("random", "ties", "equal", "special")] +
+                         [(*c, v) for c in EVICT_LONG for v in ("random", "ties")])
 def test_evict(lens, Hkv, d, page, page_out, keep, recent, dtype, values):
     from exact_io_aware_57_b200 import attn
 
-    if max(lens) > 20000 and values not in ("ties", "random"):
-        pytest.skip("the long case runs on two of the value kinds")
     g = torch.Generator().manual_seed(4)
     B, cap = len(lens), max(lens) + 3
     cache = Cache(lens, Hkv, d, page, dtype, stale=7.0)
@@ -487,3 +508,66 @@ def test_evict_that_does_not_fit():
     assert new.tolist() == [50, 20] and torch.all(kept[0] == -1)
     assert kept[1, 0].tolist() == list(range(20)) + [-1] * 10
     assert torch.equal(ko[2, 3].cpu(), cache.rows_k[1][3]) and torch.all(ko[0] == 9.0)
+
+
+def test_refusals_of_the_binding():
+    """Tensors that are not as the call needs them, each named in the error."""
+    from exact_io_aware_57_b200 import attn
+
+    cache = Cache([40, 20], 2, 64, 16, BF, room=8)
+    k, v, lens, table = cache.gpu()
+    q = torch.zeros(2, 3, 4, 64, dtype=BF, device="cuda")
+    kn = torch.zeros(2, 3, 2, 64, dtype=BF, device="cuda")
+    w = torch.zeros(2, 2, 64, device="cuda")
+    lse = torch.zeros(2, 4, 3, device="cuda")
+    i64 = lens.long()
+    for match, call in [
+        ("q must be contiguous", lambda: attn.attn_fwd_tree(q.transpose(1, 2).transpose(1, 2)[:, ::2], k, v, lens)),
+        ("cache_lens must be torch.int32", lambda: attn.attn_fwd_tree(q, k, v, i64, block_table=table)),
+        ("block_table must be torch.int32", lambda: attn.attn_fwd_tree(q, k, v, lens, block_table=table.long())),
+        ("k_cache must be torch.bfloat16", lambda: attn.attn_fwd_tree(q, k.float(), v, lens, block_table=table)),
+        ("v_cache must have shape", lambda: attn.attn_fwd_tree(q, k, v[:-1], lens, block_table=table)),
+        ("k_new must have shape", lambda: attn.attn_fwd_tree(q, k, v, lens, k_new=kn[:, :2].contiguous(), v_new=kn)),
+        ("k_cache must be \\[pages", lambda: attn.attn_fwd_tree(q[..., :32].contiguous(), k, v, lens)),
+        ("tree_mask must be torch.int64", lambda: attn.attn_fwd_tree(q, k, v, lens, k_new=kn, v_new=kn, block_table=table,
+                                                                    tree_mask=torch.zeros(3, 1, device="cuda"))),
+        ("tree_mask must have shape", lambda: attn.attn_fwd_tree(q, k, v, lens, k_new=kn, v_new=kn, block_table=table,
+                                                                 tree_mask=torch.zeros(3, 2, dtype=torch.int64,
+                                                                                       device="cuda"))),
+        ("row_lens is on cpu", lambda: attn.attn_fwd_tree(q, k, v, lens, block_table=table, row_lens=lens.cpu())),
+        ("out must be torch.bfloat16", lambda: attn.attn_fwd_tree(q, k, v, lens, block_table=table, out=q.float())),
+        ("error -3", lambda: attn.attn_fwd_tree(q, k, v, lens, block_table=table,
+                                                workspace=torch.zeros(512, dtype=torch.uint8, device="cuda"))),
+        ("unsupported dtype", lambda: attn.attn_fwd_tree(q.half(), k.half(), v.half(), lens, block_table=table)),
+        ("error -1", lambda: attn.attn_fwd_tree(q[:, :, :3].contiguous(), k, v, lens, block_table=table)),
+        ("lse must be torch.float32", lambda: attn.attn_cache_weights(q, lse.double(), k, lens, w, block_table=table)),
+        ("weights must have shape", lambda: attn.attn_cache_weights(q, lse, k, lens, w[:, :1].contiguous(), out=w,
+                                                                    block_table=table)),
+        ("rows must have shape", lambda: attn.attn_cache_append(kn, kn, k, v, lens, block_table=table, rows=lens)),
+        ("v_new must have shape", lambda: attn.attn_cache_append(kn, kn[:1], k, v, lens, block_table=table)),
+        ("error -1", lambda: attn.attn_cache_append(kn, kn, k, v, lens, block_table=table, new_lens=lens)),
+        ("error -1", lambda: attn.attn_cache_evict(k, v, w, lens, 4, k, v, block_table=table, out_table=table)),
+        ("kept must have shape", lambda: attn.attn_cache_evict(k, v, w, lens, 4, k.clone(), v.clone(), block_table=table,
+                                                               out_table=table, kept=torch.zeros(2, 2, 5,
+                                                                                                 dtype=torch.int32,
+                                                                                                 device="cuda"))),
+    ]:
+        with pytest.raises(attn.AttnError, match=match):
+            call()
+    status_ok()
+
+
+def test_on_a_stream_of_the_callers():
+    """stream=: the call runs there, and what it made lives until it has."""
+    from exact_io_aware_57_b200 import attn
+
+    cache = Cache([700, 900], 2, 128, 16, BF)
+    k, v, lens, table = cache.gpu()
+    q = torch.randn(2, 1, 8, 128, device="cuda").bfloat16()
+    want, want_lse = attn.attn_fwd_tree(q, k, v, lens, block_table=table)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = [attn.attn_fwd_tree(q, k, v, lens, block_table=table, stream=side) for _ in range(5)]
+    side.synchronize()
+    for o, lse in got:  # the same work in the same order
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
