@@ -461,7 +461,13 @@ def _dims(t, name, n):
 
 
 def _stream_on(stream, dev) -> int:
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    # (the handle alone: a Stream object takes 1.2 us to make)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _out(t, name, dtype, shape, dev, fresh):
+    """Address of an output: the caller's, checked, or one made here."""
+    return t.data_ptr() if fresh else _ptr(t, name, dtype, shape, dev)
 
 
 def _used_on(stream, *tensors):
@@ -506,12 +512,13 @@ def attn_cache_append(k_new, v_new, k_cache, v_cache, cache_lens, block_table=No
     with here:
         c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, dt, dev)
         rp, width, lp = _row_args(rows, row_lens, B, T, dev)
-        if new_lens is None:
+        fresh = new_lens is None
+        if fresh:
             new_lens = torch.empty_like(cache_lens)
             _used_on(stream, new_lens)
         _check(_lib.attn_cache_append(_ptr(k_new, "k_new", dt, shape, dev), _ptr(v_new, "v_new", dt, shape, dev),
                                       ctypes.byref(c), rp, width, lp,
-                                      _ptr(new_lens, "new_lens", torch.int32, (B,), dev), B, T, Hkv, d,
+                                      _out(new_lens, "new_lens", torch.int32, (B,), dev, fresh), B, T, Hkv, d,
                                       _dtype_code(k_new), _stream_on(stream, dev)))
     return new_lens
 
@@ -549,15 +556,18 @@ def attn_fwd_tree(q, k_cache, v_cache, cache_lens, k_new=None, v_new=None, block
             else:
                 mp = _ptr(tree_mask, "tree_mask", torch.int64, (T, words), dev)
         lp = None if row_lens is None else _ptr(row_lens, "row_lens", torch.int32, (B,), dev)
-        o = torch.empty_like(q) if out is None else out
-        if lse is None:
+        qp = _ptr(q, "q", dt, shape, dev)
+        fresh_o, fresh_lse = out is None, lse is None
+        o = torch.empty_like(q) if fresh_o else out
+        if fresh_lse:
             lse = q.new_empty((B, Hq, T), dtype=torch.float32)
         code = _dtype_code(q)
         workspace, wp, wbytes = _scratch(workspace, q, dev, _tree_size, B, Hq, Hkv, T, d, code)
         _used_on(stream, o, lse, workspace)
-        _check(_lib.attn_fwd_tree(_ptr(q, "q", dt, shape, dev), kp, vp, ctypes.byref(c), mp, mstride, lp,
-                                  _ptr(o, "out", dt, shape, dev), _ptr(lse, "lse", torch.float32, (B, Hq, T), dev), B,
-                                  Hq, Hkv, T, d, scale, wp, wbytes, code, _stream_on(stream, dev)))
+        _check(_lib.attn_fwd_tree(qp, kp, vp, ctypes.byref(c), mp, mstride, lp,
+                                  _out(o, "out", dt, shape, dev, fresh_o),
+                                  _out(lse, "lse", torch.float32, (B, Hq, T), dev, fresh_lse), B, Hq, Hkv, T, d,
+                                  scale, wp, wbytes, code, _stream_on(stream, dev)))
     return o, lse
 
 
@@ -614,17 +624,18 @@ def attn_cache_evict(k_cache, v_cache, weights, cache_lens, keep, k_out, v_out, 
         src = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, dt, dev)
         dst = _cache(k_out, v_out, None, out_table, B, Hkv, d, dt, dev, name="out")
         wp = _ptr(weights, "weights", torch.float32, (B, Hkv, cap), dev)
-        if weights_out is None:
+        fresh_w, fresh_kept, fresh_lens = weights_out is None, kept is None, new_lens is None
+        if fresh_w:
             weights_out = torch.empty_like(weights)
-        if kept is None:
+        if fresh_kept:
             kept = weights.new_empty((B, Hkv, keep), dtype=torch.int32)
-        if new_lens is None:
+        if fresh_lens:
             new_lens = torch.empty_like(cache_lens)
         _used_on(stream, weights_out, kept, new_lens)
         _check(_lib.attn_cache_evict(ctypes.byref(src), wp, cap, keep, recent, ctypes.byref(dst),
-                                     _ptr(weights_out, "weights_out", torch.float32, wshape, dev),
-                                     _ptr(kept, "kept", torch.int32, (B, Hkv, keep), dev),
-                                     _ptr(new_lens, "new_lens", torch.int32, (B,), dev), B, Hkv, d,
+                                     _out(weights_out, "weights_out", torch.float32, wshape, dev, fresh_w),
+                                     _out(kept, "kept", torch.int32, (B, Hkv, keep), dev, fresh_kept),
+                                     _out(new_lens, "new_lens", torch.int32, (B,), dev, fresh_lens), B, Hkv, d,
                                      _dtype_code(k_cache), _stream_on(stream, dev)))
     return weights_out, kept, new_lens
 
