@@ -708,7 +708,10 @@ RowTiles row_tiles(int Hq, int Hkv, int Nq) {
   return r;
 }
 
-// @@ measured
+// Rows up to which the transposed kernel (tree_few_sm100.cu) is taken.  At 4 rows, 64
+// sequences: 204 us against 219 here at 300 .. 8191 slots, 78 against 96 at 1024, 50
+// against 67 at about 250.  A transposed form of 32 rows took 152 us against 130 here at
+// 8 tokens of 4 heads: its P and O columns cost more than the rows that are padding here.
 constexpr int kFewRows = 16;
 
 // Two slots per worker (the unit its run begins in, the unit it ends in): few rows,

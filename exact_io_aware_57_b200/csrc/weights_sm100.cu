@@ -7,8 +7,12 @@
 // sum stays in a register, and nothing is reduced across threads.  With the LSE
 // at hand there is no running maximum: each score costs one FMA, one
 // exponential and one addition.  A decode step has few rows and is bound by
-// reading K; a prompt is bound by the exponentials (16 a cycle and SM against
-// 64 scores of 128-wide dot products on the tensor cores).
+// reading K (32 sequences of 8191 slots, 8 KV heads: 72 us for 330 MB); a prompt by
+// the exponentials (16 a cycle and SM against 32 scores of 128-wide dot products on
+// the tensor cores: 8192 tokens of 32 heads in 341 us, 239 of them the exponentials
+// alone).  Measured there and not kept: a quarter of the exponentials as polynomials
+// (355 us: four warps per scheduler do not hide their chains), two issuing threads
+// (357: 80 registers a thread, spills), each Q tile kept for two key tiles (341).
 //
 // Work.  A unit is one (sequence, KV head, 128-key tile); its steps are the row
 // tiles (up to 128 rows: tt counted rows x gb heads) from the first that sees
@@ -18,8 +22,8 @@
 //
 //   warps 0..15  sums: warpgroup g takes the steps g, g + 4, ... of the run, thread
 //                r key r (with two warpgroups the exponentials' unit stood idle
-//                half the time behind TMEM reads and barriers: an 8192-token
-//                prompt took 485 us instead of @@ us)
+//                half the time behind TMEM reads and barriers: that prompt took
+//                485 us instead of 457, before the producers below were split)
 //   warp 16      TMEM owner + single-thread tcgen05.mma issuer
 //   warp 17      TMA producer of K tiles, through the page table
 //   warp 18      producer of Q tiles: TMA, or copies by the row list
