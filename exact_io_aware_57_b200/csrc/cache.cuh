@@ -58,8 +58,8 @@ ATTN_DEVINL long long cache_row(const CacheView& c, int b, int s, int* status) {
 // ---- equal runs.  The work of a launch is a line of `total` steps, sequence b
 // owning cost(b) of them.  It is cut into equal runs, one per worker; a block has
 // LANES workers, blockIdx + lane * gridDim, so that with few steps every block
-// has its first worker busy.  At most `total` workers take part: worker w then
-// takes the steps [run0, run1), beginning `off` steps into sequence b.
+// has its first worker busy.  No more workers take part than have steps: worker w
+// then takes the steps [run0, run1), beginning `off` steps into sequence b.
 struct Run {
   long long run0, run1, off;
   int b;
@@ -84,10 +84,10 @@ ATTN_DEVINL long long run_begin(long long total, int workers, int w) {
   return w * total / workers;
 }
 
-// Leaves the block's runs in s.runs.  All THREADS threads of the block take part;
+// Leaves the block's runs in s.runs, of `least` steps at least if there are that many.  All THREADS threads of the block take part;
 // the block is synchronised on return.
 template <int THREADS, int LANES, class Cost>
-ATTN_DEVINL void find_runs(RunSmem<THREADS, LANES>& s, int B, Cost cost) {
+ATTN_DEVINL void find_runs(RunSmem<THREADS, LANES>& s, int B, int least, Cost cost) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // inclusive sum over the block's threads; all: their total
   auto scan = [&](long long x, long long& all) {
@@ -115,7 +115,7 @@ ATTN_DEVINL void find_runs(RunSmem<THREADS, LANES>& s, int B, Cost cost) {
     scan(b < B ? cost(b) : 0, all);
     total += all;
   }
-  const int workers = (int)min((long long)gridDim.x * LANES, total);
+  const int workers = (int)min((long long)gridDim.x * LANES, max(total / least, min(total, 1ll)));
   long long run0[LANES];
 #pragma unroll
   for (int l = 0; l < LANES; ++l) {

@@ -188,6 +188,7 @@ struct TreeParams {
   int num_splits;
   float *o_part, *lse_part;  // fp32 path: as SplitKV's; bf16 path: raw O, and (m, l) pairs
   int part_tiles;            // bf16 path: row tiles of a partial (1 or 2)
+  int unit_cost;             // bf16 path: tiles that a unit's ends count for (tree.cuh)
   TreeCut* cuts;             // one per worker
   int* status;
   long long wait_limit;

@@ -8,15 +8,15 @@
 namespace attn {
 
 constexpr int kTreeKeys = 128;  // keys per tile
-// Steps that a unit counts for beyond its tiles when the work is cut into runs: its
-// first and last tiles, Q and O cost about as much as this many others (with 0,
-// the workers whose runs hold several short units end last: 16 sequences of 2000 ..
-// 12345 slots with 32 tokens each took 145 us instead of 136; 2 to 8 measured equal).
-constexpr int kUnitCost = 4;
-
+// The work is cut into runs by steps.  A key tile is one step for each of the unit's
+// row tiles: two row tiles' softmax takes twice one's (counted alike, the workers of
+// sequences that fill one row tile ended after half the others' time: 16 sequences
+// of up to 61 tokens took 184 us instead of 169).  And each row tile counts for
+// unit_cost tiles more, as its first and last tiles, Q and O cost: otherwise the
+// workers whose runs hold several short units end last.
 // One sequence's share of the work: per KV head `active` units (pairs of row
-// tiles; with one row tile in all, that one) of n tiles and kUnitCost steps, then
-// the units whose rows are all padding (one empty step each).
+// tiles; of an odd number the last by itself) of n tiles, then the units whose rows
+// are all padding (one empty step each).
 struct TreeSeq {
   int len, nr, nc, n, row_tiles, active;
   long long per_head;
@@ -30,7 +30,7 @@ ATTN_DEVINL TreeSeq tree_seq(const TreeParams& p, const RowTiles& rw, int b) {
   s.n = s.nc + (p.k_new ? (s.nr + kTreeKeys - 1) / kTreeKeys : 0);
   s.row_tiles = s.n > 0 ? (s.nr + rw.tt - 1) / rw.tt * rw.gblk : 0;
   s.active = (s.row_tiles + 1) / 2;
-  s.per_head = (long long)s.active * (s.n + kUnitCost) + ((rw.tiles + 1) / 2 - s.active);
+  s.per_head = (long long)s.row_tiles * (s.n + p.unit_cost) + ((rw.tiles + 1) / 2 - s.active);
   return s;
 }
 
@@ -38,11 +38,12 @@ ATTN_DEVINL TreeSeq tree_seq(const TreeParams& p, const RowTiles& rw, int b) {
 struct TreeUnit {
   int b, hk, pair;  // row tiles 2 pair, 2 pair + 1
   int tb, te, n;    // tiles [tb, te) of n
+  int rest;         // steps from the run's end to its last tile's first (and that one)
   bool two, empty;  // two row tiles; no row of it sees anything
 };
 
 struct TreeWalk {
-  int b, hk, pair, step;  // the next step (tiles first, then kUnitCost without one)
+  int b, hk, pair, step;  // the next step (the tiles' first, then those without one)
   int left;               // steps left in the run
   TreeSeq s;
 
@@ -52,10 +53,10 @@ struct TreeWalk {
     b = run.b;
     s = tree_seq(p, rw, b);
     hk = (int)(run.off / s.per_head);
-    const int cost = s.n + kUnitCost;
-    const long long off = run.off - hk * s.per_head, busy = (long long)s.active * cost;
+    const long long cost = 2ll * (s.n + p.unit_cost);
+    const long long off = run.off - hk * s.per_head, busy = (long long)s.row_tiles * (s.n + p.unit_cost);
     pair = off < busy ? (int)(off / cost) : s.active + (int)(off - busy);
-    step = off < busy ? (int)(off - (long long)pair * cost) : 0;
+    step = off < busy ? (int)(off - pair * cost) : 0;
   }
   ATTN_DEVINL bool next(const TreeParams& p, const RowTiles& rw, TreeUnit& u) {
     while (left > 0) {
@@ -67,13 +68,17 @@ struct TreeWalk {
         }
       }
       const bool empty = pair >= s.active;
-      const int n = empty ? 1 : s.n, end = min(empty ? 1 : s.n + kUnitCost, step + left);
-      const int tb = step, te = min(n, end);
+      const int shift = !empty && 2 * pair + 1 < s.row_tiles;  // log2 of the steps per tile
+      const int n = empty ? 1 : s.n, end = min(empty ? 1 : (s.n + p.unit_cost) << shift, step + left);
+      // a tile belongs to the run that has its first step (runs are two steps at least
+      // where tiles are: every run inside the tiles has one)
+      const int tb = (step + shift) >> shift, te = min(n, (end + shift) >> shift);
       u.b = b;
       u.hk = hk;
       u.pair = pair++;
       u.empty = empty;
-      u.two = !empty && 2 * u.pair + 1 < s.row_tiles;
+      u.two = shift;
+      u.rest = ((n - 1) << shift) + 1 - end;
       left -= end - step;
       step = 0;
       if (tb < te) {

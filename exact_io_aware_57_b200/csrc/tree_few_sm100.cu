@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc_fence_before();
-  find_runs<kThreads, 2>(s.run, p.B, [&](int b) { return tree_seq(p, rw, b).per_head * p.Hkv; });
+  find_runs<kThreads, 2>(s.run, p.B, 1, [&](int b) { return tree_seq(p, rw, b).per_head * p.Hkv; });
   tc_fence_after();
   const Runs<2>& runs = s.run.runs;
   const uint32_t tmem = s.tmem_base;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (r == 0) {
       TreeCut cut{0, 0, 0, 0, 0};
       if (ok && run.run1 > run.run0 && u.tb == 0 && u.te < u.n)
-        cut = TreeCut{u.b, u.hk, u.pair, 1, run_parts(runs.total, runs.workers, worker, run.run1, u.n - u.te)};
+        cut = TreeCut{u.b, u.hk, u.pair, 1, run_parts(runs.total, runs.workers, worker, run.run1, u.rest)};
       p.cuts[worker] = cut;
     }
   }

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
-  find_runs<kThreads, 1>(s.run, p.B, [&](int b) { return tree_seq(p, rw, b).per_head * p.Hkv; });
+  find_runs<kThreads, 1>(s.run, p.B, rw.tiles > 1 ? 2 : 1, [&](int b) { return tree_seq(p, rw, b).per_head * p.Hkv; });
   tc_fence_after();
   const Runs<1>& runs = s.run.runs;
   const Run& run = runs.lane[0];
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     TreeCut cut{0, 0, 0, 0, 0};
     if (!s.abort_flag && run.run1 > run.run0 && u.tb == 0 && u.te < u.n)
-      cut = TreeCut{u.b, u.hk, u.pair, u.two ? 2 : 1, run_parts(runs.total, runs.workers, blockIdx.x, run.run1, u.n - u.te)};
+      cut = TreeCut{u.b, u.hk, u.pair, u.two ? 2 : 1, run_parts(runs.total, runs.workers, blockIdx.x, run.run1, u.rest)};
     p.cuts[blockIdx.x] = cut;
   }
 }
@@ -713,6 +713,12 @@ RowTiles row_tiles(int Hq, int Hkv, int Nq) {
 // against 67 at about 250.  A transposed form of 32 rows took 152 us against 130 here at
 // 8 tokens of 4 heads: its P and O columns cost more than the rows that are padding here.
 constexpr int kFewRows = 16;
+// Tiles that a unit's ends count for in the two kernels.  Here 16 sequences of 2000 ..
+// 12345 slots with up to 61 tokens took 169 us with 4, 163 with 6, 157 with 8, 163 with
+// 12; 32 tokens 145 with 0 and 136 with 2 to 8.  The other kernel's two workers per
+// CTA cover for each other: 4 sequences of 16 heads with two rows took 26 us with 4,
+// 27 .. 35 with 6 to 12.
+constexpr int kUnitCost = 8, kFewUnitCost = 4;
 
 // Two slots per worker (the unit its run begins in, the unit it ends in): few rows,
 // two workers per CTA and one row tile; else one worker and one or two.
@@ -781,6 +787,7 @@ int launch_tree_sm100(TreeParams p, void* workspace, cudaStream_t st) {
   const Layout a = layout(p.Hq, p.Hkv, p.Nq, p.D);
   p.rw = a.rw;
   p.part_tiles = a.part_tiles;
+  p.unit_cost = a.workers > sm_count() ? kFewUnitCost : kUnitCost;
   p.wait_limit = kWaitLimitCycles;
   char* ws = static_cast<char*>(workspace);
   p.o_part = reinterpret_cast<float*>(ws);
