@@ -599,6 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       step = s0 + n;
       if (n > 1) {  // several warpgroups took steps
+        // The previous unit's sums have been read.  All of them wait for that, the
+        // owner too: it may have been among those that handed theirs over, and the
+        // others of that unit may still be at it, whose phase it must not skip.
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.part_empty, (shared & 1) ^ 1, ab));
+        if (!ok) break;
         if (owner) {
           ok = __all_sync(0xffffffffu, mbar_wait(&s.part_full, shared & 1, ab));
           if (!ok) break;
@@ -606,8 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.part_empty);
         } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(&s.part_empty, (shared & 1) ^ 1, ab));
-          if (!ok) break;
           s.part[wg][r] = sum;
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.part_full);

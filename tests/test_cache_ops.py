@@ -215,6 +215,45 @@ def test_weights(lens, Hq, Hkv, d, page, T, accepted, extra, inplace, dtype):
     within(out, ref, tol, "weights")
 
 
+@pytest.mark.parametrize("d,Hkv,group", [(64, 2, 4), (128, 1, 8), (64, 4, 5)])
+@pytest.mark.parametrize("lens,counts", [
+    # chunks at the ends of sequences: units of many and of one or two steps in one run
+    ([8701, 3695, 4337, 328, 1187, 4313, 6386, 2628, 4324], [1376, 318, 562, 58, 764, 516, 432, 672, 1270]),
+    ([700, 0, 129, 1300, 64, 700, 257], [700, 0, 129, 65, 64, 1, 130]),
+    ([2049], [2049]),
+])
+def test_weights_of_chunks(lens, counts, d, Hkv, group):
+    """Several row tiles per head, units shared by CTAs and warpgroups; the reference in
+    64 bits on the GPU, its bound that of weights_ref."""
+    from exact_io_aware_57_b200 import attn
+
+    g = torch.Generator().manual_seed(9)
+    B, n, scale = len(lens), max(counts), 1.0 / math.sqrt(d)
+    cache = Cache(lens, Hkv, d, 128, BF)
+    k, _, cl, table = cache.gpu()
+    q = torch.randn(B, n, Hkv * group, d, generator=g).to(BF).cuda()
+    ref = torch.rand(B, Hkv, max(lens), generator=g).double().cuda()
+    tol = 2.0 ** -22 * ref
+    w, lse = ref.float(), torch.full((B, Hkv * group, n), -math.inf, device="cuda")
+    ref = w.double()
+    for b, (m, c) in enumerate(zip(lens, counts)):
+        rows = cache.rows_k[b].double().cuda()
+        hide = torch.arange(m, device="cuda")[None, :] > (m - c + torch.arange(c, device="cuda"))[:, None]
+        for h in range(Hkv * group if c else 0):
+            kh, qh = rows[:, h // group], q[b, :c, h].double()
+            s = (qh @ kh.T * scale).masked_fill(hide, -math.inf)
+            lse[b, h, :c] = torch.logsumexp(s, 1).float()
+            p = torch.exp(s - lse[b, h, :c].double()[:, None])
+            e = (d + 2) * 2.0 ** -24 * scale * (qh.abs() @ kh.abs().T) + 1e-5
+            ref[b, h // group, :m] += p.sum(0)
+            tol[b, h // group, :m] += (p * (e + 2.0 ** -22)).sum(0)
+    for _ in range(3):  # the order in which warpgroups finish varies
+        out = attn.attn_cache_weights(q, lse, k, cl, w, block_table=table, out=torch.empty_like(w),
+                                      row_lens=torch.tensor(counts, dtype=torch.int32).cuda())
+        status_ok()
+        within(out, ref.cpu(), tol.cpu(), "weights")
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_weights_of_a_prompt_sum_to_its_rows(dtype):
     """From zeros (weights None): every row hands out one unit per head."""
