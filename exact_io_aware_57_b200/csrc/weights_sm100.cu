@@ -709,6 +709,10 @@ int launch_t(const WeightsParams& p, cudaStream_t st) {
   const int ctas = sm_count();
   weights_kernel<D><<<ctas, kThreads, smem, st>>>(mk, mq, p, form);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (rw.tiles == 1 && p.weights == p.out) {  // no unit is cut, no slot left to copy
+    count_launch();
+    return ATTN_OK;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = p.weights == p.out ? dim3((unsigned)ctas)
                                    : dim3((unsigned)std::max((long long)ctas, (long long)p.B * p.Hkv),
