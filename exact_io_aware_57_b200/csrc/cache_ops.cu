@@ -320,7 +320,7 @@ int launch_evict(const EvictParams& p, cudaStream_t st) {
       cudaSuccess)
     return ATTN_ERR_CUDA;
   if (cudaLaunchKernelEx(&cfg, choose_kernel, p) != cudaSuccess) return ATTN_ERR_CUDA;
-  const long long rows = (long long)p.keep * p.Hkv;
+  const long long rows = (long long)std::min(p.keep, p.cap) * p.Hkv;  // (len <= cap)
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)((rows + kGatherRows - 1) / kGatherRows), (unsigned)p.B);
