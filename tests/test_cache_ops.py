@@ -95,6 +95,16 @@ def test_tree_at_every_place_of_a_tile(T, shape, d, page):
              BF, [int(x) for x in rng.integers(0, T + 1, len(lens))])
 
 
+@pytest.mark.parametrize("T,Hq,d", [(61, 8, 128), (130, 8, 64), (33, 16, 128), (200, 6, 64)])
+@pytest.mark.parametrize("longest", [300, 2500])
+def test_tree_row_tiles_side_by_side(T, Hq, d, longest):
+    """Sequences that fill no, one, an odd or an even number of row tiles, so that runs
+    begin and end at every place of a unit."""
+    rng = np.random.default_rng(T + longest)
+    lens = [int(x) for x in rng.integers(0, longest, 17)]
+    run_tree(Cache(lens, 2, d, 32, BF), Hq, T, "tree", BF, [int(rng.choice([0, 1, T // 4, T // 2 + 1, T])) for _ in lens])
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_tree_rows_without_any_key(dtype):
     """A mask that leaves a row empty, over an empty and over a used cache."""
