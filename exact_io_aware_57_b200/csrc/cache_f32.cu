@@ -121,16 +121,25 @@ __global__ void __launch_bounds__(32 * ROWS) tree_f32_kernel(TreeParams p) {
     p.lse_part[(((long long)split * p.B + b) * p.Hq + h) * p.Nq + t] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
-template <int D>
-__global__ void __launch_bounds__(32 * ROWS) weights_f32_kernel(WeightsParams p) {
-  constexpr int S = D + 4;
-  __shared__ float ks[KT * S], part[ROWS][KT];
+// Weights.  A block has 32 slots, a lane each; its warps take AT (row, head)s at a
+// time.  Four in 16 warps, so that a key read from shared memory serves four dot
+// products and four rows' loads are on their way at once: a prompt of 606 tokens of 3
+// heads on one KV head takes 196 us, with one at a time in 8 warps 655.  One in 8 warps
+// where these have two rows each at most, as in a decode step, whose time is the
+// latency of a row (4 sequences of 800 .. 1000 slots, 16 heads on 8: 12 us, the other
+// way 29).
+constexpr int weights_warps(int at) { return at == 1 ? 8 : 16; }
+
+template <int D, int AT>
+__global__ void __launch_bounds__(32 * weights_warps(AT)) weights_f32_kernel(WeightsParams p) {
+  constexpr int S = D + 4, kWarps = weights_warps(AT);
+  __shared__ float ks[KT * S], part[kWarps][KT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv, hk = blockIdx.y, b = blockIdx.z, base = blockIdx.x * KT;
   int len, nr;
   if (!cache_len(p.c, b, p.cap, p.status, len) || !row_count(p.row_lens, b, p.max_rows, p.status, nr)) return;
   const int n = min(KT, len - base);  // slots of this tile in use (may be negative)
-  for (int i = threadIdx.x; i < KT * (D / 4); i += 32 * ROWS) {
+  for (int i = threadIdx.x; i < KT * (D / 4); i += 32 * kWarps) {
     const int key = i / (D / 4), c = 4 * (i % (D / 4));
     float4 kk = make_float4(0.f, 0.f, 0.f, 0.f);
     if (key < n) {
@@ -142,25 +151,39 @@ __global__ void __launch_bounds__(32 * ROWS) weights_f32_kernel(WeightsParams p)
   __syncthreads();
   float acc = 0.f;
   if (n > 0) {
-    const int first = max(0, base - (len - nr));  // earlier rows see no slot of this tile
-    for (int i = first * G + warp; i < nr * G; i += ROWS) {
-      const int row = i / G, h = hk * G + i % G;
-      const int t = p.rows ? p.rows[(long long)b * p.max_rows + row] : row;
-      if (t < 0 || t >= p.Nq) {
-        if (lane == 0) atomicExch(p.status, ATTN_ERR_INVALID);
-        continue;
+    const long long first = (long long)max(0, base - (len - nr)) * G;  // earlier rows see no slot of this tile
+    for (long long i0 = first + warp * AT; i0 < (long long)nr * G; i0 += kWarps * AT) {
+      const float* q[AT];
+      float z[AT], s[AT];
+      int last[AT];  // the last slot that the row sees
+#pragma unroll
+      for (int x = 0; x < AT; ++x) {
+        const int row = (int)((i0 + x) / G), h = hk * G + (int)((i0 + x) % G);
+        int t = row;
+        bool on = row < nr;
+        if (on && p.rows) t = p.rows[(long long)b * p.max_rows + row];
+        if (on && (t < 0 || t >= p.Nq)) {
+          if (lane == 0) atomicExch(p.status, ATTN_ERR_INVALID);
+          on = false;
+        }
+        q[x] = static_cast<const float*>(p.q) + (on ? (((long long)b * p.Nq + t) * p.Hq + h) * D : 0);
+        z[x] = on ? p.lse[((long long)b * p.Hq + h) * p.Nq + t] : -INFINITY;
+        last[x] = len - nr + row;
+        s[x] = 0.f;
       }
-      const float* q = static_cast<const float*>(p.q) + (((long long)b * p.Nq + t) * p.Hq + h) * D;
-      const float z = p.lse[((long long)b * p.Hq + h) * p.Nq + t];
-      float s = 0.f;
-#pragma unroll 8
+#pragma unroll(AT > 1 ? 4 : 16)
       for (int c = 0; c < D; c += 4) {
-        const float4 a = load4(q + c);
         const float4 k = *reinterpret_cast<const float4*>(&ks[lane * S + c]);
-        s = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, s))));
+#pragma unroll
+        for (int x = 0; x < AT; ++x) {
+          const float4 a = load4(q[x] + c);
+          s[x] = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, s[x]))));
+        }
       }
       // a row without a visible key (LSE = -inf) weighs nothing
-      if (lane < n && base + lane <= len - nr + row && z != -INFINITY) acc += expf(s * p.scale - z);
+#pragma unroll
+      for (int x = 0; x < AT; ++x)
+        if (lane < n && base + lane <= last[x] && z[x] != -INFINITY) acc += expf(s[x] * p.scale - z[x]);
     }
   }
   part[warp][lane] = acc;
@@ -170,7 +193,7 @@ __global__ void __launch_bounds__(32 * ROWS) weights_f32_kernel(WeightsParams p)
     const long long at = ((long long)b * p.Hkv + hk) * p.cap + j;
     float w = p.weights ? p.weights[at] : 0.f, sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) sum += part[i][lane];
+    for (int i = 0; i < kWarps; ++i) sum += part[i][lane];
     if (lane < n) w += sum;
     p.out[at] = w;
   }
@@ -197,7 +220,10 @@ int launch_tree_f32(const TreeParams& p, cudaStream_t st) {
 
 int launch_weights_f32(const WeightsParams& p, cudaStream_t st) {
   const dim3 grid((unsigned)((p.cap + KT - 1) / KT), (unsigned)p.Hkv, (unsigned)p.B);
-  (p.D == 64 ? weights_f32_kernel<64> : weights_f32_kernel<128>)<<<grid, 32 * ROWS, 0, st>>>(p);
+  const bool few = (long long)p.max_rows * (p.Hq / p.Hkv) <= 2 * weights_warps(1);
+  const auto kernel = p.D == 64 ? (few ? weights_f32_kernel<64, 1> : weights_f32_kernel<64, 4>)
+                                : (few ? weights_f32_kernel<128, 1> : weights_f32_kernel<128, 4>);
+  kernel<<<grid, 32 * weights_warps(few ? 1 : 4), 0, st>>>(p);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
