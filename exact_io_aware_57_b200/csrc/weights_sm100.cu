@@ -9,8 +9,8 @@
 // exponential and one addition.  A decode step has few rows and is bound by
 // reading K (32 sequences of 8191 slots, 8 KV heads: 72 us for 330 MB); a prompt by
 // the exponentials (16 a cycle and SM against 32 scores of 128-wide dot products on
-// the tensor cores: 8192 tokens of 32 heads in 341 us, 239 of them the exponentials
-// alone).  Measured there and not kept: a quarter of the exponentials as polynomials
+// the tensor cores: 8192 tokens of 32 heads in 325 us, 239 of them the exponentials
+// alone).  Measured when that was 341 and not kept: a quarter of the exponentials as polynomials
 // (355 us: four warps per scheduler do not hide their chains), two issuing threads
 // (357: 80 registers a thread, spills), each Q tile kept for two key tiles (341).
 //
