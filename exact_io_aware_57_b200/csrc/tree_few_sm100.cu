@@ -67,6 +67,10 @@ constexpr uint32_t kTmemCols = 64;
 constexpr int W = 16;  // rows there is room for, the columns of the products
 constexpr float kRaise = 64.f;   // log2 units: P stays below 2^64
 constexpr float kNoKey = 1e30f;  // -m of a row that has seen no key: any score raises it
+// -m of a column that is no row, or a row that does not count: its x - m is -inf or NaN
+// whatever its scores are (of Q rows in shared memory that no load wrote, or of a
+// caller's padding), so that it never raises the references of the others.
+constexpr float kNoRow = -INFINITY;
 
 template <int D>
 struct FewSmem {
@@ -434,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && w.next(p, rw, u)) {
       const int n = u.te - u.tb, len = w.s.len, nr = w.s.nr, nc = w.s.nc;
+      const int counted = nr * rw.gb;  // rows of the unit that count
       const bool mine = !u.empty;
       uint64_t sums[W / 2];  // this thread's keys' share of l, by pairs of rows
 #pragma unroll
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < W; ++e) {
               const float x = __uint_as_float(v[e]) * sc;
-              neg_m[e] = x == -INFINITY ? kNoKey : -x;
+              neg_m[e] = e >= counted ? kNoRow : x == -INFINITY ? kNoKey : -x;
             }
           }
           if (!(ok = meet())) break;
@@ -497,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = old;
 #pragma unroll
             for (int x = 0; x < 4; ++x) m = fmaxf(m, parts[x * W + r]);
-            factor[r] = old == -INFINITY ? 0.f : ex2(old - m);
-            neg_m[r] = m == -INFINITY ? kNoKey : -m;
+            factor[r] = r >= counted || old == -INFINITY ? 0.f : ex2(old - m);
+            neg_m[r] = r >= counted ? kNoRow : m == -INFINITY ? kNoKey : -m;
           }
           if (!(ok = meet())) break;
           fetch_nm();
