@@ -96,9 +96,10 @@ __global__ void __launch_bounds__(32 * ROWS) tree_f32_kernel(TreeParams p) {
       see = mrow ? (mrow[j >> 6] >> (j & 63)) & 1 : j <= t;
     }
     s = see ? s * p.scale : -INFINITY;
+    // (a score of NaN leaves m as it is and l at NaN, which the row keeps)
     const float m_new = fmaxf(m, warp_max(s));
-    if (m_new == -INFINITY) continue;
-    const float alpha = expf(m - m_new), w = see ? expf(s - m_new) : 0.f;
+    const float ref = m_new == -INFINITY ? 0.f : m_new;
+    const float alpha = expf(m - ref), w = see ? expf(s - ref) : 0.f;
     l = l * alpha + warp_sum(w);
     m = m_new;
 #pragma unroll
@@ -112,13 +113,14 @@ __global__ void __launch_bounds__(32 * ROWS) tree_f32_kernel(TreeParams p) {
     }
   }
   if (!valid) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const bool none = l == 0.f;  // sees no key
+  const float inv = none ? 0.f : 1.f / l;
   const long long at = (long long)b * p.Nq + t;
   float* o = p.o_part + ((long long)split * p.B * p.Nq + at) * p.Hq * D + (long long)h * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = acc[e] * inv;
+  for (int e = 0; e < E; ++e) o[e] = none ? 0.f : acc[e] * inv;
   if (lane == 0)
-    p.lse_part[(((long long)split * p.B + b) * p.Hq + h) * p.Nq + t] = l > 0.f ? m + logf(l) : -INFINITY;
+    p.lse_part[(((long long)split * p.B + b) * p.Hq + h) * p.Nq + t] = none ? -INFINITY : m + logf(l);
 }
 
 // Weights.  A block has 32 slots, a lane each; its warps take AT (row, head)s at a

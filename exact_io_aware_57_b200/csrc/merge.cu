@@ -5,7 +5,8 @@
 // not need the matrix", "Carry the Normalizer": the carried (m, l, a) state
 // suffices to resume the softmax exactly), applied to whole partials:
 //   m = max_t LSE_t,  w_t = exp(LSE_t - m),  O = sum_t w_t O_t / sum_t w_t,
-//   LSE = m + ln sum_t w_t;  rows with every LSE_t = -inf give O = 0, LSE = -inf.
+//   LSE = m + ln sum_t w_t;  rows with every LSE_t = -inf give O = 0, LSE = -inf,
+// and a NaN in any LSE_t (a score that was NaN) makes the row NaN.
 // HBM-bound: one warp per output row reads num_parts * D * 4 bytes.
 #include "common.cuh"
 #include "kernels.h"
@@ -27,14 +28,20 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ o_
   const int i = (int)(bi % Nq), b = (int)(bi / Nq);
   const long long li = ((long long)b * Hq + h) * Nq + i;
   float m = -INFINITY;
-  for (int t = 0; t < T; ++t) m = fmaxf(m, __ldg(lse_part + t * lse_stride + li));
+  bool any = false;  // (a NaN is not in the maximum, but is something)
+  for (int t = 0; t < T; ++t) {
+    const float x = __ldg(lse_part + t * lse_stride + li);
+    m = fmaxf(m, x);
+    any |= x != -INFINITY;
+  }
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   float l = 0.f;
-  if (m != -INFINITY) {
+  if (any) {
+    const float ref = m == -INFINITY ? 0.f : m;
     for (int t = 0; t < T; ++t) {
-      const float w = expf(__ldg(lse_part + t * lse_stride + li) - m);
+      const float w = expf(__ldg(lse_part + t * lse_stride + li) - ref);
       l += w;
       const float* src = o_part + t * o_stride + row * D + lane * E;
       if constexpr (E == 4) {
@@ -50,7 +57,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ o_
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
   if constexpr (OUT_F32) {
     float* dst = static_cast<float*>(o) + row * D + lane * E;
 #pragma unroll
@@ -63,7 +71,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ o_
       *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
     }
   }
-  if (lane == 0) lse[li] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (lane == 0) lse[li] = none ? -INFINITY : m + logf(l);
 }
 
 }  // namespace

@@ -69,3 +69,136 @@ def test_results_do_not_depend_on_the_call_before(d):
         seen.append(tree_bits(q, cache))
     for o, lse in seen[1:]:
         assert torch.equal(o, seen[0][0]) and torch.equal(lse, seen[0][1])
+
+
+# ------------------------------------------------- values that are not finite
+def tree_call(q, rows, kn, vn, see):
+    """A cache of the rows (lists of K, V per sequence), the call, O and LSE on the CPU."""
+    from exact_io_aware_57_b200 import attn
+
+    rows_k, rows_v = rows
+    cache = Cache([x.shape[0] for x in rows_k], kn.shape[2], q.shape[3], 16, q.dtype)
+    for b, x in enumerate(rows_k):
+        for s in range(x.shape[0]):
+            cache.k[cache.at(b, s)], cache.v[cache.at(b, s)] = x[s], rows_v[b][s]
+    k, v, lens, table = cache.gpu()
+    o, lse = attn.attn_fwd_tree(q.cuda(), k, v, lens, k_new=kn.cuda(), v_new=vn.cuda(), block_table=table,
+                                tree_mask=mask_words(np.stack(see)).cuda())
+    status_ok()
+    return o.cpu().float(), lse.cpu()
+
+
+def check_nan(got, ref, bad, lost=torch.isnan):
+    """bad [B, T, Hq]: rows that are NaN (`lost`) throughout; the others within their bounds."""
+    o, lse = got
+    o_r, l_r, tol_o, tol_l = ref
+    bl = bad.transpose(1, 2)
+    assert torch.equal(lost(o), bad[..., None].expand_as(o))
+    assert torch.equal(lost(lse), bl)
+    within(torch.where(bad[..., None], 0.0, o), torch.where(bad[..., None], 0.0, o_r), tol_o.nan_to_num(1.0), "o")
+    within(torch.where(bl, 0.0, lse), torch.where(bl, 0.0, l_r), tol_l.nan_to_num(1.0), "lse")
+
+
+SIZES = [(3, 8, BF), (40, 8, BF), (70, 16, BF), (3, 8, F32), (20, 4, F32)]
+
+
+def nan_case(T, Hq, dtype, lens=(900, 33, 130)):
+    g, rng = torch.Generator().manual_seed(7), np.random.default_rng(7)
+    B, Hkv, d = len(lens), 2, 64
+    q = torch.randn(B, T, Hq, d, generator=g).to(dtype)
+    kn, vn = (torch.randn(B, T, Hkv, d, generator=g).to(dtype) for _ in range(2))
+    rows = [[torch.randn(n, Hkv, d, generator=g).to(dtype) for n in lens] for _ in range(2)]
+    see = [random_tree(T, rng) for _ in range(B)]
+    return q, rows, kn, vn, see, torch.zeros(B, T, Hq, dtype=torch.bool)
+
+
+def ref_of(q, rows, kn, vn, see):
+    B, T, _, d = q.shape
+    return tree_ref(q, rows[0], rows[1], kn, vn, see, [T] * B, 1 / math.sqrt(d))
+
+
+@on_gpu
+@pytest.mark.parametrize("T,Hq,dtype", SIZES)
+def test_nan_in_a_row_of_q(T, Hq, dtype):
+    q, rows, kn, vn, see, bad = nan_case(T, Hq, dtype)
+    ref = ref_of(q, rows, kn, vn, see)
+    for b, t, h in ((0, 1, 2), (1, 0, 0), (2, T - 1, Hq - 1)):
+        q[b, t, h, 5], bad[b, t, h] = math.nan, True
+    check_nan(tree_call(q, rows, kn, vn, see), ref, bad)
+
+
+@on_gpu
+@pytest.mark.parametrize("T,Hq,dtype", SIZES)
+def test_nan_in_cached_keys(T, Hq, dtype):
+    """One slot, a whole tile's slots, all slots: every row that sees them is NaN."""
+    q, rows, kn, vn, see, bad = nan_case(T, Hq, dtype)
+    ref = ref_of(q, rows, kn, vn, see)
+    rows[0][0][513, 0, 3] = math.nan
+    rows[0][1][:, 1] = math.nan
+    rows[0][2][0, 0, 0] = math.nan
+    G = Hq // 2
+    bad[0, :, :G] = bad[1, :, G:] = bad[2, :, :G] = True
+    check_nan(tree_call(q, rows, kn, vn, see), ref, bad)
+
+
+@on_gpu
+@pytest.mark.parametrize("T,Hq,dtype", SIZES)
+def test_nan_in_a_new_key(T, Hq, dtype):
+    """Rows that do not see it are as ever."""
+    q, rows, kn, vn, see, bad = nan_case(T, Hq, dtype, lens=(900, 0, 130))
+    ref = ref_of(q, rows, kn, vn, see)
+    for b in range(3):
+        kn[b, 1, 1, 7] = math.nan
+        bad[b, :, Hq // 2:] = torch.from_numpy(see[b][:, 1].copy())[:, None]
+    assert bad.any() and not bad[:, :, Hq // 2:].all()
+    check_nan(tree_call(q, rows, kn, vn, see), ref, bad)
+
+
+@on_gpu
+@pytest.mark.parametrize("T,Hq,dtype", SIZES)
+def test_infinite_scores(T, Hq, dtype):
+    """A key of one infinite component: score -inf weighs nothing, +inf leaves no answer."""
+    q, rows, kn, vn, see, bad = nan_case(T, Hq, dtype)
+    q[..., 9] = torch.where(q[..., 9] < 0, -0.5, 0.5).to(dtype)
+    rows[0][0][700, 0, 9] = math.inf
+    rows[0][1][2, 1, 9] = -math.inf
+    G = Hq // 2
+    bad[0, :, :G] = q[0, :, :G, 9] > 0
+    bad[1, :, G:] = q[1, :, G:, 9] < 0
+    # rows at -inf have the answer of a cache without that slot, the other heads any finite one
+    whole = [[x.nan_to_num(posinf=0.0, neginf=0.0) for x in r] for r in rows]
+    ref = ref_of(q, whole, kn, vn, see)
+    for b, s, h0 in ((0, 700, 0), (1, 2, G)):
+        less = [[torch.cat([x[:s], x[s + 1:]]) if i == b else x for i, x in enumerate(r)] for r in whole]
+        for x, y in zip(ref, ref_of(q, less, kn, vn, see)):
+            if x.shape[1] == T:
+                x[b, :, h0:h0 + G] = y[b, :, h0:h0 + G]
+            else:
+                x[b, h0:h0 + G] = y[b, h0:h0 + G]
+    check_nan(tree_call(q, rows, kn, vn, see), ref, bad, lambda x: ~torch.isfinite(x))
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_merge_keeps_nan(dtype):
+    """A partial of NaN makes its row NaN; partials that saw nothing (whatever their O holds
+    where all did) give zeros."""
+    from exact_io_aware_57_b200 import attn
+
+    g = torch.Generator().manual_seed(5)
+    o = torch.randn(3, 1, 4, 2, 64, generator=g)
+    lse = torch.randn(3, 1, 2, 4, generator=g)
+    want, want_lse = attn.attn_merge_partials(o.cuda(), lse.cuda(), out_dtype=dtype)
+    lse[1, 0, 0, 1] = lse[:, 0, 1, 2] = lse[0, 0, 1, 0] = math.nan
+    lse[1:, 0, 1, 0] = -math.inf
+    lse[:, 0, 0, 3], o[:, 0, 3, 0] = -math.inf, math.nan
+    got, got_lse = attn.attn_merge_partials(o.cuda(), lse.cuda(), out_dtype=dtype)
+    status_ok()
+    bad = torch.tensor([[False, True, False, False], [True, False, True, False]]).cuda()
+    gone = torch.tensor([[False, False, False, True], [False] * 4]).cuda()
+    assert torch.equal(torch.isnan(got_lse[0]), bad)
+    assert torch.equal(torch.isnan(got[0]), bad.T[..., None].expand_as(got[0]))
+    assert torch.all(got[0].transpose(0, 1)[gone] == 0) and torch.all(got_lse[0][gone] == -math.inf)
+    keep = ~(bad | gone)
+    assert torch.equal(got_lse[0][keep], want_lse[0][keep])
+    assert torch.equal(got[0].transpose(0, 1)[keep], want[0].transpose(0, 1)[keep])
