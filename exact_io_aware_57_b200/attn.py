@@ -6,6 +6,10 @@ output tensors with PyTorch (device memory and streams are PyTorch's), and
 calls the C entry points of the same names.  Every step of the attention path
 runs in the library's CUDA kernels; there is no fallback.  If the library is
 missing, importing this module raises.
+
+``stream`` (default: the current one) is where a call runs.  Another stream than
+the current one does not wait for it: the inputs have to be ready there, and the
+outputs are, once it has been waited for.
 """
 from __future__ import annotations
 
@@ -445,12 +449,20 @@ def _row_args(rows, row_lens, B, n, dev):
 _HERE = contextlib.nullcontext()
 
 
-def _on(t, name):
-    """t's device index, and a context in which that device is the current one."""
+def _on(t, name, stream):
+    """t's device index, a context in which that device and the caller's `stream` (None:
+    the current one) are current, and the stream that was current, where it is not that.
+
+    What a call allocates it allocates inside: memory of the current stream may still be
+    in use there by work that has not run, and the caller's stream does not wait for it."""
     dev = t.get_device()
     if dev < 0:
         raise AttnError(f"{name} must be a CUDA tensor")
-    return dev, _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream is None:
+        return dev, _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev), None
+    if stream.device.index != dev:
+        raise AttnError(f"stream is on {stream.device}, {name} on cuda:{dev}")
+    return dev, torch.cuda.stream(stream), torch.cuda.current_stream(dev)
 
 
 def _dims(t, name, n):
@@ -470,11 +482,13 @@ def _out(t, name, dtype, shape, dev, fresh):
     return t.data_ptr() if fresh else _ptr(t, name, dtype, shape, dev)
 
 
-def _used_on(stream, *tensors):
-    """Tensors made for a call on a stream that is not the current one outlive it there."""
+def _used_on(stream, caller, *tensors):
+    """Outputs and workspaces of a call on a stream of the caller's: their memory is not
+    given out again before what uses them there, and on the stream that was current, has run."""
     if stream is not None:
         for t in tensors:
             t.record_stream(stream)
+            t.record_stream(caller)
 
 
 def _scratch(workspace, like, dev, size_of, *args):
@@ -508,14 +522,14 @@ def attn_cache_append(k_new, v_new, k_cache, v_cache, cache_lens, block_table=No
     lengths, int32 [B], in a buffer of their own; cache_lens is not changed."""
     B, T, Hkv, d = shape = _dims(k_new, "k_new", 4)
     dt = k_new.dtype
-    dev, here = _on(k_new, "k_new")
+    dev, here, caller = _on(k_new, "k_new", stream)
     with here:
         c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, dt, dev)
         rp, width, lp = _row_args(rows, row_lens, B, T, dev)
         fresh = new_lens is None
         if fresh:
             new_lens = torch.empty_like(cache_lens)
-            _used_on(stream, new_lens)
+            _used_on(stream, caller, new_lens)
         _check(_lib.attn_cache_append(_ptr(k_new, "k_new", dt, shape, dev), _ptr(v_new, "v_new", dt, shape, dev),
                                       ctypes.byref(c), rp, width, lp,
                                       _out(new_lens, "new_lens", torch.int32, (B,), dev, fresh), B, T, Hkv, d,
@@ -542,7 +556,7 @@ def attn_fwd_tree(q, k_cache, v_cache, cache_lens, k_new=None, v_new=None, block
         raise AttnError("pass k_new and v_new together")
     if tree_mask is not None and k_new is None:
         raise AttnError("tree_mask needs k_new and v_new")
-    dev, here = _on(q, "q")
+    dev, here, caller = _on(q, "q", stream)
     with here:
         c = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, dt, dev)
         new = (B, T, Hkv, d)
@@ -563,7 +577,7 @@ def attn_fwd_tree(q, k_cache, v_cache, cache_lens, k_new=None, v_new=None, block
             lse = q.new_empty((B, Hq, T), dtype=torch.float32)
         code = _dtype_code(q)
         workspace, wp, wbytes = _scratch(workspace, q, dev, _tree_size, B, Hq, Hkv, T, d, code)
-        _used_on(stream, o, lse, workspace)
+        _used_on(stream, caller, o, lse, workspace)
         _check(_lib.attn_fwd_tree(qp, kp, vp, ctypes.byref(c), mp, mstride, lp,
                                   _out(o, "out", dt, shape, dev, fresh_o),
                                   _out(lse, "lse", torch.float32, (B, Hq, T), dev, fresh_lse), B, Hq, Hkv, T, d,
@@ -586,7 +600,7 @@ def attn_cache_weights(q, lse, k_cache, cache_lens, weights, block_table=None, r
     B, T, Hq, d = shape = _dims(q, "q", 4)
     Hkv, dt = _dims(k_cache, "k_cache", 4)[2], q.dtype
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    dev, here = _on(q, "q")
+    dev, here, caller = _on(q, "q", stream)
     with here:
         c = _cache(k_cache, None, cache_lens, block_table, B, Hkv, d, dt, dev)
         rp, width, lp = _row_args(rows, row_lens, B, T, dev)
@@ -599,7 +613,7 @@ def attn_cache_weights(q, lse, k_cache, cache_lens, weights, block_table=None, r
         wp = None if weights is None else _ptr(weights, "weights", torch.float32, (B, Hkv, cap), dev)
         code = _dtype_code(q)
         workspace, sp, sbytes = _scratch(workspace, q, dev, _weights_size, B, Hq, Hkv, d, code)
-        _used_on(stream, out, workspace)
+        _used_on(stream, caller, out, workspace)
         _check(_lib.attn_cache_weights(_ptr(q, "q", dt, shape, dev), _ptr(lse, "lse", torch.float32, (B, Hq, T), dev),
                                        ctypes.byref(c), rp, width, lp, wp, op, cap, B, Hq, Hkv, T, d, scale, sp, sbytes,
                                        code, _stream_on(stream, dev)))
@@ -619,7 +633,7 @@ def attn_cache_evict(k_cache, v_cache, weights, cache_lens, keep, k_out, v_out, 
     keep, recent = int(keep), int(recent)
     if not 0 <= recent <= keep or keep == 0:
         raise AttnError("need 0 <= recent <= keep and keep > 0")
-    dev, here = _on(k_cache, "k_cache")
+    dev, here, caller = _on(k_cache, "k_cache", stream)
     with here:
         src = _cache(k_cache, v_cache, cache_lens, block_table, B, Hkv, d, dt, dev)
         dst = _cache(k_out, v_out, None, out_table, B, Hkv, d, dt, dev, name="out")
@@ -631,7 +645,7 @@ def attn_cache_evict(k_cache, v_cache, weights, cache_lens, keep, k_out, v_out, 
             kept = weights.new_empty((B, Hkv, keep), dtype=torch.int32)
         if fresh_lens:
             new_lens = torch.empty_like(cache_lens)
-        _used_on(stream, weights_out, kept, new_lens)
+        _used_on(stream, caller, weights_out, kept, new_lens)
         _check(_lib.attn_cache_evict(ctypes.byref(src), wp, cap, keep, recent, ctypes.byref(dst),
                                      _out(weights_out, "weights_out", torch.float32, wshape, dev, fresh_w),
                                      _out(kept, "kept", torch.int32, (B, Hkv, keep), dev, fresh_kept),

@@ -202,3 +202,85 @@ def test_merge_keeps_nan(dtype):
     keep = ~(bad | gone)
     assert torch.equal(got_lse[0][keep], want_lse[0][keep])
     assert torch.equal(got[0].transpose(0, 1)[keep], want[0].transpose(0, 1)[keep])
+
+
+# ------------------------------------------------- streams of the caller's
+def cache_calls():
+    """Name -> (a call of one operator on a given stream, outputs and workspace its own)."""
+    from exact_io_aware_57_b200 import attn
+
+    g = torch.Generator().manual_seed(8)
+    cache = Cache([700, 900], 2, 128, 16, BF, room=4)
+    k, v, lens, table = cache.gpu()
+    q, kn, vn = (torch.randn(2, 1, h, 128, generator=g).to(BF).cuda() for h in (8, 2, 2))
+    lse = torch.randn(2, 8, 1, generator=g).cuda() + 7
+    w = torch.rand(2, 2, 1000, generator=g).cuda()
+    ko, vo = torch.zeros(2, 64, 2, 128, dtype=BF, device="cuda"), torch.zeros(2, 64, 2, 128, dtype=BF, device="cuda")
+    return {
+        "tree": lambda s: attn.attn_fwd_tree(q, k, v, lens, k_new=kn, v_new=vn, block_table=table, stream=s),
+        "append": lambda s: (attn.attn_cache_append(kn, vn, k, v, lens, block_table=table, stream=s),),
+        "weights": lambda s: (attn.attn_cache_weights(q, lse, k, lens, None, block_table=table, stream=s),),
+        "evict": lambda s: attn.attn_cache_evict(k, v, w, lens, 64, ko, vo, block_table=table, stream=s),
+    }
+
+
+def check_streams(call):
+    """No output or workspace of a call on a side stream lies in memory that work still
+    pending on the current stream is about to write or read."""
+    want = [x.clone() for x in call(None)]
+    side = torch.cuda.Stream()
+    warm = [call(side) for _ in range(8)]
+    # blocks of every size, freed while the current stream has yet to write them
+    junk = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (512, 4096, 1 << 16, 1 << 20, 1 << 22, 1 << 25)
+            for _ in range(4)]
+    for x in junk:
+        x.fill_(1)  # (what is done for the first time may wait for the device)
+    torch.cuda._sleep(1)
+    torch.cuda.synchronize()
+    del warm
+    torch.cuda._sleep(2_000_000_000)  # about a second
+    for x in junk:
+        x.fill_(255)
+    spans = [(x.data_ptr(), x.data_ptr() + x.numel()) for x in junk]
+    del junk, x
+    got = call(side)
+    for t in got:
+        assert not any(lo < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < hi for lo, hi in spans)
+    # what reads an output on the current stream is pending when the output is freed
+    copies = [x.clone() for x in got]
+    spans = [(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size()) for x in got]
+    del got, t
+    again = [x for _ in range(3) for x in call(side)]
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()
+    for t in again:
+        assert not any(lo < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < hi for lo, hi in spans)
+    torch.cuda.synchronize()
+    for x, y in zip(copies, want):
+        assert torch.equal(x, y)
+    for i, x in enumerate(again):
+        assert torch.equal(x, want[i % len(want)])
+
+
+@on_gpu
+@pytest.mark.parametrize("name", ["tree", "append", "weights", "evict"])
+def test_memory_of_a_call_on_a_side_stream(name):
+    check_streams(cache_calls()[name])
+    status_ok()
+
+
+class FakeStream:
+    device = torch.device("cuda", 1)
+
+
+def test_stream_of_another_device_is_refused():
+    """A tensor that says it is on device 0 and a stream of device 1, without a GPU."""
+    from exact_io_aware_57_b200 import attn
+
+    class OnDevice0:
+        @staticmethod
+        def get_device():
+            return 0
+
+    with pytest.raises(attn.AttnError, match="stream is on cuda:1, q on cuda:0"):
+        attn._on(OnDevice0, "q", FakeStream)
