@@ -16,6 +16,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import inspect
 import math
 from pathlib import Path
 
@@ -131,6 +132,30 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+def _on_its_stream(call):
+    """A call that, given ``stream``, allocates its outputs and workspaces on that stream:
+    memory of the current one may still be in use there by work that has not run.  Its
+    outputs are not given out again before what uses them on the current stream has run."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return call(*args, **kwargs)
+        caller = torch.cuda.current_stream()
+        if stream.device != caller.device:
+            raise AttnError(f"stream is on {stream.device}, the current device is {caller.device}")
+        with torch.cuda.stream(stream):
+            out = call(*args, **kwargs)
+        for t in out if isinstance(out, tuple) else (out,):
+            t.record_stream(stream)
+            t.record_stream(caller)
+        return out
+
+    return run
+
+
 def _bias_args(bias, B, Hq, Nq, Nk):
     if bias is None:
         return None, 0
@@ -157,6 +182,7 @@ def _window_args(window, bias):
     return (-1 if wl is None else int(wl)), (-1 if wr is None else int(wr))
 
 
+@_on_its_stream
 def attn_fwd(q, k, v, bias=None, causal=False, scale=None, out=None, lse=None, stream=None, alibi_slopes=None,
              window=None):
     """O, LSE = attention(q [B,Nq,Hq,d], k/v [B,Nk,Hkv,d]); o like q, lse fp32 [B,Hq,Nq].
@@ -189,6 +215,7 @@ def attn_fwd(q, k, v, bias=None, causal=False, scale=None, out=None, lse=None, s
     return o, lse
 
 
+@_on_its_stream
 def attn_fwd_dv(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None):
     """Forward with V of its own width: q/k [..., d], v [B,Nk,Hkv,d_v] -> o [B,Nq,Hq,d_v]."""
     B, Nq, Hq, d = q.shape
@@ -201,6 +228,7 @@ def attn_fwd_dv(q, k, v, causal=False, scale=None, out=None, lse=None, stream=No
     return o, lse
 
 
+@_on_its_stream
 def attn_bwd_dv(q, k, v, o, lse, dout, causal=False, scale=None, workspace=None, dq=None, dk=None, dv=None,
                 stream=None):
     """Backward of attn_fwd_dv: q/k/dq/dk width d, v/o/dout/dv width d_v."""
@@ -224,6 +252,7 @@ def attn_selftest_wait_timeout(limit_cycles=1_000_000, stream=None) -> None:
     _check(_lib.attn_selftest_wait_timeout(int(limit_cycles), _stream(stream)))
 
 
+@_on_its_stream
 def attn_selftest_ex2(x, stream=None):
     """2^x by the kernels' FMA-pipe exponential (fp32 device tensor in, same out)."""
     if x.dtype != torch.float32 or not x.is_contiguous():
@@ -241,6 +270,7 @@ def attn_splitkv_workspace_size(batch, h_q, n_q, d, num_splits) -> int:
     return int(_lib.attn_splitkv_workspace_size(batch, h_q, n_q, d, num_splits))
 
 
+@_on_its_stream
 def attn_fwd_splitkv(q, k, v, causal=False, scale=None, num_splits=0, out=None, lse=None, workspace=None,
                      stream=None):
     """attn_fwd computed over num_splits key ranges and merged (bf16, dense)."""
@@ -259,6 +289,7 @@ def attn_fwd_splitkv(q, k, v, causal=False, scale=None, num_splits=0, out=None, 
     return o, lse
 
 
+@_on_its_stream
 def attn_fwd_partial(q, k, v, causal=False, scale=None, o_part=None, lse_part=None, stream=None):
     """Unmerged attention of q [B,Nq,Hq,d] over one key block k/v [B,Nk,Hkv,d] (bf16):
     o_part fp32 [B,Nq,Hq,d] (normalised over the block) and lse_part fp32 [B,Hq,Nq].
@@ -277,6 +308,7 @@ def attn_fwd_partial(q, k, v, causal=False, scale=None, o_part=None, lse_part=No
     return o_part, lse_part
 
 
+@_on_its_stream
 def attn_quantize_e4m3(x, x8=None, scales=None, stream=None):
     """Per-(batch, head) e4m3 quantisation of x bf16 [B,N,H,d]: returns x8 (uint8
     e4m3 bytes, same layout) and scales fp32 [B,H] (amax / 448)."""
@@ -290,6 +322,7 @@ def attn_quantize_e4m3(x, x8=None, scales=None, stream=None):
     return x8, scales
 
 
+@_on_its_stream
 def attn_fwd_fp8(q8, q_scales, k8, k_scales, v, causal=False, scale=None, out=None, lse=None, stream=None):
     """Forward with S = Q8 K8^T on e4m3 tensor cores (see attn_quantize_e4m3), P V in
     bf16: o bf16 [B,Nq,Hq,d], lse fp32 [B,Hq,Nq].  d = 128."""
@@ -306,6 +339,7 @@ def attn_fwd_fp8(q8, q_scales, k8, k_scales, v, causal=False, scale=None, out=No
     return o, lse
 
 
+@_on_its_stream
 def attn_merge_partials(o_parts, lse_parts, out=None, lse=None, out_dtype=torch.bfloat16, stream=None):
     """Merge fp32 partials o_parts [T,B,Nq,Hq,d], lse_parts [T,B,Hq,Nq] over disjoint key ranges."""
     if o_parts.dtype != torch.float32 or lse_parts.dtype != torch.float32:
@@ -325,6 +359,7 @@ def attn_bwd_workspace_size(batch, h_q, n_q, d) -> int:
     return int(_lib.attn_bwd_workspace_size(batch, h_q, n_q, d))
 
 
+@_on_its_stream
 def attn_bwd(q, k, v, o, lse, dout, bias=None, causal=False, scale=None, workspace=None, dq=None, dk=None,
              dv=None, stream=None, alibi_slopes=None, window=None):
     """dq, dk, dv of attn_fwd for upstream gradient dout (layouts as q, k, v)."""
@@ -363,6 +398,7 @@ def attn_bwd(q, k, v, o, lse, dout, bias=None, causal=False, scale=None, workspa
     return dq, dk, dv
 
 
+@_on_its_stream
 def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal=False, scale=None,
                     out=None, lse=None, stream=None):
     """Packed forward: q [Tq,Hq,d], k/v [Tk,Hkv,d], cu_seqlens int32 device; lse [Hq,Tq]."""
@@ -380,6 +416,7 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqle
     return o, lse
 
 
+@_on_its_stream
 def attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal=False,
                     scale=None, workspace=None, dq=None, dk=None, dv=None, stream=None):
     """Backward of attn_fwd_varlen: dq like q [Tq,Hq,d], dk/dv like k/v [Tk,Hkv,d]."""
@@ -658,6 +695,7 @@ def attn_naive_scratch_size(n_q, n_k) -> int:
     return int(_lib.attn_naive_scratch_size(n_q, n_k))
 
 
+@_on_its_stream
 def attn_fwd_naive(q, k, v, causal=False, scale=None, scratch=None, stream=None):
     """Materialising three-step forward (measurement comparator only)."""
     B, Nq, Hq, d = q.shape
