@@ -350,6 +350,8 @@ int attn_cache_append(const void* k_new, const void* v_new, const attn_kv_cache*
  * do all rows of a sequence whose length or count is not acceptable.
  * The value rows of cached slots and of new keys j < row_lens[b] take part in
  * matrix products with P = 0 where a row does not see them: they must be finite.
+ * (bf16: P is at most 2^8 and P V is summed in fp32, so |V| times the number of keys
+ * has to stay below 2^119.)  A score of NaN or +inf makes its row NaN.
  * n_q <= 4096; tree_mask 8-byte aligned.  workspace: DEVICE, 256-byte aligned,
  * attn_fwd_tree_workspace_size(...) bytes for the current device (bf16: 40 MB at
  * most, whatever the batch and the lengths), contents need not be initialised;

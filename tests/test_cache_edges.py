@@ -204,6 +204,30 @@ def test_merge_keeps_nan(dtype):
     assert torch.equal(got[0].transpose(0, 1)[keep], want[0].transpose(0, 1)[keep])
 
 
+# ------------------------------------------------- large values
+@on_gpu
+@pytest.mark.parametrize("T,Hq", [(1, 4), (4, 8), (40, 8)])
+@pytest.mark.parametrize("rise", [6, 20, 40])
+def test_large_values_after_a_low_first_score(T, Hq, rise):
+    """|V| near 2^100 behind a first key whose scores are `rise` (log2 units) lower: the
+    weights must not carry the sums out of fp32's range."""
+    g = torch.Generator().manual_seed(12)
+    n, d, Hkv = 600, 128, 2
+    q = torch.full((1, T, Hq, d), 0.25).to(BF)
+    rows_k = [0.02 * torch.randn(n, Hkv, d, generator=g)]
+    # scores of 0 but the first: -rise ln 2
+    rows_k[0][0] = -rise * math.log(2) * math.sqrt(d) / (0.25 * d)
+    rows_k = [rows_k[0].to(BF)]
+    rows_v = [(torch.randn(n, Hkv, d, generator=g) * 2.0 ** 100).to(BF)]
+    kn, vn = torch.zeros(1, T, Hkv, d).to(BF), (torch.randn(1, T, Hkv, d, generator=g) * 2.0 ** 100).to(BF)
+    see = [np.tril(np.ones((T, T), dtype=bool))]
+    rows = (rows_k, rows_v)
+    o, lse = tree_call(q, rows, kn, vn, see)
+    o_r, l_r, tol_o, tol_l = ref_of(q, rows, kn, vn, see)
+    within(o, o_r, tol_o, "o")
+    within(lse, l_r, tol_l, "lse")
+
+
 # ------------------------------------------------- streams of the caller's
 def cache_calls():
     """Name -> (a call of one operator on a given stream, outputs and workspace its own)."""
