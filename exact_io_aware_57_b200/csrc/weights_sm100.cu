@@ -646,9 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Blocks (c < ctas, 0) add the parts of the unit whose first part CTA c holds, in
-// CTA order.  When out is another buffer than weights, block (u, y) copies the
-// y-th run of the slots of (sequence, KV head) u that no unit covers (behind the
-// sequence's end); it need not wait for that.
+// CTA order.  When out is another buffer than weights, block (u, y) copies every
+// gridDim.y-th run, from the y-th on, of the slots of (sequence, KV head) u that no unit
+// covers (behind the sequence's end); it need not wait for that.
 constexpr int kFinish = 256, kCopyRun = 8 * kFinish;
 
 __global__ void __launch_bounds__(kFinish) weights_finish_kernel(const WeightsParams p, const int ctas) {
@@ -658,19 +658,21 @@ __global__ void __launch_bounds__(kFinish) weights_finish_kernel(const WeightsPa
     const int b = blockIdx.x / p.Hkv;
     // a sequence that is not acceptable is left as it is
     if (cache_len(p.c, b, p.cap, p.status, len) && row_count(p.row_lens, b, p.max_rows, p.status, cnt)) {
-      const int from = cnt > 0 ? len : 0, j0 = blockIdx.y * kCopyRun + r;
+      const int from = cnt > 0 ? len : 0;
       const float* src = p.weights ? p.weights + (long long)blockIdx.x * p.cap : nullptr;
       float* dst = p.out + (long long)blockIdx.x * p.cap;
-      float x[kCopyRun / kFinish];
+      for (int j0 = blockIdx.y * kCopyRun + r; j0 < p.cap; j0 += gridDim.y * kCopyRun) {
+        float x[kCopyRun / kFinish];
 #pragma unroll
-      for (int i = 0; i < kCopyRun / kFinish; ++i) {
-        const int j = j0 + i * kFinish;
-        x[i] = src && j >= from && j < p.cap ? src[j] : 0.f;
-      }
+        for (int i = 0; i < kCopyRun / kFinish; ++i) {
+          const int j = j0 + i * kFinish;
+          x[i] = src && j >= from && j < p.cap ? src[j] : 0.f;
+        }
 #pragma unroll
-      for (int i = 0; i < kCopyRun / kFinish; ++i) {
-        const int j = j0 + i * kFinish;
-        if (j >= from && j < p.cap) dst[j] = x[i];
+        for (int i = 0; i < kCopyRun / kFinish; ++i) {
+          const int j = j0 + i * kFinish;
+          if (j >= from && j < p.cap) dst[j] = x[i];
+        }
       }
     }
   }
@@ -716,7 +718,7 @@ int launch_t(const WeightsParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = p.weights == p.out ? dim3((unsigned)ctas)
                                    : dim3((unsigned)std::max((long long)ctas, (long long)p.B * p.Hkv),
-                                          (unsigned)((p.cap + kCopyRun - 1) / kCopyRun));
+                                          (unsigned)std::min((p.cap + kCopyRun - 1) / kCopyRun, 65535));
   cfg.blockDim = dim3(kFinish);
   cfg.stream = st;
   cudaLaunchAttribute attr{};

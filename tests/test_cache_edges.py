@@ -228,6 +228,25 @@ def test_large_values_after_a_low_first_score(T, Hq, rise):
     within(lse, l_r, tol_l, "lse")
 
 
+# ------------------------------------------------- largest sizes
+@on_gpu
+@pytest.mark.parametrize("cap", [134215681, 1 << 28])
+def test_weights_of_the_largest_capacity(cap):
+    """Slots behind a short sequence's end, to the most that there can be."""
+    from exact_io_aware_57_b200 import attn
+
+    g = torch.Generator().manual_seed(1)
+    cache = Cache([5], 1, 64, 8, BF)
+    k, _, cl, table = cache.gpu()
+    q, lse = torch.randn(1, 1, 2, 64, generator=g).to(BF), torch.full((1, 2, 1), 2.0)
+    w = torch.arange(cap, device="cuda", dtype=F32).remainder_(251).view(1, 1, cap)
+    out = attn.attn_cache_weights(q.cuda(), lse.cuda(), k, cl, w, block_table=table, out=torch.empty_like(w))
+    status_ok()
+    assert torch.equal(out[..., 5:], w[..., 5:])
+    ref, tol = weights_ref(q, lse, cache.rows_k, w[..., :5].cpu(), [[0]], [1], 0.125)
+    within(out[..., :5], ref, tol, "weights")
+
+
 # ------------------------------------------------- streams of the caller's
 def cache_calls():
     """Name -> (a call of one operator on a given stream, outputs and workspace its own)."""
