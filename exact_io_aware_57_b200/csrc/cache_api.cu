@@ -1,6 +1,7 @@
 // C-ABI entry points of the key/value cache (declared in include/attn.h):
 // argument validation, workspace carving and dispatch by dtype.
 #include <algorithm>
+#include <climits>
 
 #include "cache.cuh"
 #include "kernels.h"
@@ -22,6 +23,7 @@ int check_sizes(int batch, int h_q, int h_kv, int d, int dtype) {
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (dtype != ATTN_BF16 && dtype != ATTN_F32) return ATTN_ERR_UNSUPPORTED;
   if (h_q > 65535 || batch > 65535) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)batch * h_kv > INT_MAX) return ATTN_ERR_UNSUPPORTED;  // (a block per sequence and KV head)
   return ATTN_OK;
 }
 

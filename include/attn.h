@@ -309,8 +309,8 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float*
  * stated with each call; behind a page number out of range its result is
  * undefined.  Rows behind lens[b] are never used, whatever they hold.
  *
- * Both dtypes are taken everywhere; at most 65535 heads or batch elements and
- * 2^28 slots per sequence.
+ * Both dtypes are taken everywhere; at most 65535 heads or batch elements, 2^31 - 1
+ * (sequence, KV head) pairs and 2^28 slots per sequence.
  */
 typedef struct attn_kv_cache {
   void* k;

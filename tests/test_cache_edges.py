@@ -247,6 +247,15 @@ def test_weights_of_the_largest_capacity(cap):
     within(out[..., :5], ref, tol, "weights")
 
 
+def test_more_sequence_heads_than_a_grid_has_are_refused():
+    from exact_io_aware_57_b200 import attn
+
+    for dtype in (BF, F32):
+        assert attn.attn_cache_weights_workspace_size(65535, 65535, 65535, 64, dtype) == 0
+        assert attn.attn_cache_weights_workspace_size(65535, 32769, 32769, 64, dtype) == 0
+        assert attn.attn_cache_weights_workspace_size(65535, 32768, 32768, 64, dtype) > 0
+
+
 # ------------------------------------------------- streams of the caller's
 def cache_calls():
     """Name -> (a call of one operator on a given stream, outputs and workspace its own)."""
