@@ -556,7 +556,8 @@ def attn_cache_append(k_new, v_new, k_cache, v_cache, cache_lens, block_table=No
     cache (k_cache / v_cache [pages, page_size, Hkv, d], cache_lens int32 [B], block_table
     int32 [B, max_pages]; without a table page b is sequence b's): slot cache_lens[b] + i
     takes row rows[b, i] (default i), i < row_lens[b] (default all).  Returns the new
-    lengths, int32 [B], in a buffer of their own; cache_lens is not changed."""
+    lengths, int32 [B], in a buffer of their own; cache_lens is not changed.  A sequence
+    that is not acceptable (attn_device_status) keeps its length."""
     B, T, Hkv, d = shape = _dims(k_new, "k_new", 4)
     dt = k_new.dtype
     dev, here, caller = _on(k_new, "k_new", stream)

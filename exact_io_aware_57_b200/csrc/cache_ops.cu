@@ -30,7 +30,9 @@ constexpr int kCopyThreads = 256;
 
 // ------------------------------------------------------------------- append
 // `lanes` threads (a power of two, a warp at most) share a row, so that one of them
-// has up to four chunks of K and of V on their way at once.
+// has up to four chunks of K and of V on their way at once.  The sequence's first block
+// looks through its row list before it states the new length: with a row that does not
+// exist the sequence keeps its length, and what the others write lies behind its end.
 __global__ void __launch_bounds__(kCopyThreads) append_kernel(AppendParams p, int lanes) {
   const int b = blockIdx.y;
   int len, n;
@@ -39,7 +41,16 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(AppendParams p, in
     atomicExch(p.status, ATTN_ERR_INVALID);
     ok = false;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.new_lens[b] = ok ? len + n : p.c.lens[b];
+  if (blockIdx.x == 0) {
+    bool bad = !ok;
+    if (ok && p.rows) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n; i += kCopyThreads)
+        bad |= (unsigned)__ldg(p.rows + (long long)b * p.max_rows + i) >= (unsigned)p.n_new;
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) p.new_lens[b] = bad ? p.c.lens[b] : len + n;
+  }
   const int per = kCopyThreads / lanes, first = threadIdx.x % lanes, chunks = p.row_bytes / 16;
   const long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;
   if (!ok || row >= n) return;

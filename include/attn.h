@@ -330,6 +330,8 @@ typedef struct attn_kv_cache {
  * accepted path of a verified tree as `rows` only accepted rows enter the
  * cache.  The table must name pages for the new slots.  A sequence whose
  * length or count is not acceptable, or whose rows do not fit, is left as it is.
+ * One whose list names a row that does not exist keeps its length too: new_lens[b]
+ * = lens[b], and rows of slots behind it may have been written.
  */
 int attn_cache_append(const void* k_new, const void* v_new, const attn_kv_cache* cache,
                       const int* rows, int max_rows, const int* row_lens, int* new_lens, int batch,
@@ -376,7 +378,8 @@ int attn_fwd_tree(const void* q, const void* k_new, const void* v_new, const att
  * [batch, h_kv, cap], cap >= lens[b]; weights NULL means zeros; out may be
  * weights.  Slots j >= lens[b] take weights' value.  The V rows are not used:
  * cache->v may be NULL.  A prompt is the case lens[b] = count = n_q.
- * A sequence whose length or count is not acceptable is left as it is in out.
+ * A sequence whose length or count is not acceptable is left as it is in out; an
+ * index in rows that names no row adds nothing, and the others count as ever.
  * workspace: as attn_fwd_tree's, attn_cache_weights_workspace_size(...) bytes.
  */
 size_t attn_cache_weights_workspace_size(int batch, int h_q, int h_kv, int d, int dtype);

@@ -256,6 +256,61 @@ def test_more_sequence_heads_than_a_grid_has_are_refused():
         assert attn.attn_cache_weights_workspace_size(65535, 32768, 32768, 64, dtype) > 0
 
 
+# ------------------------------------------------- row lists
+@on_gpu
+@pytest.mark.parametrize("n,bad", [(2, 0), (2, 1), (700, 699), (700, 300)])
+@pytest.mark.parametrize("index", [-1, 9, 10 ** 9])
+def test_append_with_a_row_that_does_not_exist(n, bad, index):
+    """The sequence's length stays, the others are appended to."""
+    from exact_io_aware_57_b200 import attn
+
+    g = torch.Generator().manual_seed(2)
+    cache = Cache([3, 10, 0], 2, 64, 16, BF, room=n, stale=7.0)
+    kn, vn = torch.randn(3, 9, 2, 64, generator=g).to(BF), torch.randn(3, 9, 2, 64, generator=g).to(BF)
+    rows = torch.randint(0, 9, (3, n), generator=g, dtype=torch.int32)
+    want = rows.clone()
+    rows[1, bad] = index
+    k, v, cl, table = cache.gpu()
+    new = attn.attn_cache_append(kn.cuda(), vn.cuda(), k, v, cl, block_table=table, rows=rows.cuda())
+    torch.cuda.synchronize()
+    assert attn.attn_device_status() == attn.ATTN_ERR_INVALID
+    assert new.tolist() == [3 + n, 10, n]
+    for b in (0, 2):
+        for i in range(n):
+            cache.k[cache.at(b, cache.lens[b] + i)] = kn[b, want[b, i]]
+            cache.v[cache.at(b, cache.lens[b] + i)] = vn[b, want[b, i]]
+    got_k, got_v = k.cpu(), v.cpu()
+    for b, m in ((0, 3 + n), (1, 10), (2, n)):
+        for s in range(m):
+            at = cache.at(b, s)
+            assert torch.equal(got_k[at], cache.k[at]) and torch.equal(got_v[at], cache.v[at])
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [3, 200])
+def test_weights_with_a_row_that_does_not_exist(dtype, T):
+    """It adds nothing; the other rows count as ever."""
+    from exact_io_aware_57_b200 import attn
+
+    g = torch.Generator().manual_seed(6)
+    cache = Cache([400, 250], 2, 64, 16, dtype)
+    k, _, cl, table = cache.gpu()
+    q = torch.randn(2, T, 4, 64, generator=g).to(dtype)
+    lse = 6 + torch.rand(2, 4, T, generator=g)
+    w = torch.rand(2, 2, 400, generator=g)
+    rows = torch.arange(T, dtype=torch.int32).repeat(2, 1)
+    rows[0, 1], rows[1, T - 1] = T, -1
+    out = attn.attn_cache_weights(q.cuda(), lse.cuda(), k, cl, w.cuda(), block_table=table, rows=rows.cuda(),
+                                  out=torch.empty_like(w).cuda())
+    torch.cuda.synchronize()
+    assert attn.attn_device_status() == attn.ATTN_ERR_INVALID
+    gone = lse.clone()
+    gone[0, :, 1] = gone[1, :, T - 1] = -math.inf
+    ref, tol = weights_ref(q, gone, cache.rows_k, w, [list(range(T))] * 2, [T, T], 0.125)
+    within(out, ref, tol, "weights")
+
+
 # ------------------------------------------------- streams of the caller's
 def cache_calls():
     """Name -> (a call of one operator on a given stream, outputs and workspace its own)."""
