@@ -663,7 +663,8 @@ def attn_cache_evict(k_cache, v_cache, weights, cache_lens, keep, k_out, v_out, 
     """Cut each sequence of a cache down to keep slots, per KV head: the last `recent` slots
     and the others of largest weight (fp32 [B,Hkv,cap]; ties: the lower slot).  They go in
     ascending order to the cache k_out / v_out (out_table), whose pages are others than the
-    source's.  Returns weights_out (like weights, zeros behind the last slot), kept int32
+    source's in use: another pool, or (out_table another table) free pages of the same one.
+    Returns weights_out (like weights, zeros behind the last slot), kept int32
     [B,Hkv,keep] (source slots, -1 behind the last) and new_lens int32 [B]."""
     _, _, Hkv, d = _dims(k_cache, "k_cache", 4)
     B, _, cap = wshape = _dims(weights, "weights", 3)

@@ -194,8 +194,12 @@ int attn_cache_evict(const attn_kv_cache* cache, const float* weights, int cap, 
     return ATTN_ERR_INVALID;
   if (!aligned(weights, 4) || !aligned(weights_out, 4) || !aligned(kept, 4) || !aligned(new_lens, 4)) return ATTN_ERR_INVALID;
   if (cap <= 0 || keep <= 0 || recent < 0 || recent > keep) return ATTN_ERR_INVALID;
-  // rows move in no order: the source has to stay as it is
-  if (cache->k == dst->k || cache->v == dst->v || cache->k == dst->v || cache->v == dst->k) return ATTN_ERR_INVALID;
+  // Rows move in no order: the source has to stay as it is.  Within one pool that takes
+  // other pages of the same size, named by another table.
+  if (cache->k == dst->v || cache->v == dst->k) return ATTN_ERR_INVALID;
+  if ((cache->k == dst->k || cache->v == dst->v) &&
+      (cache->block_table == dst->block_table || cache->page_size != dst->page_size))
+    return ATTN_ERR_INVALID;
   if (cap > kMaxSeqLen || keep > kMaxSeqLen) return ATTN_ERR_UNSUPPORTED;
   if (!supported_device()) return ATTN_ERR_UNSUPPORTED;
   p.weights = weights;

@@ -393,8 +393,10 @@ int attn_cache_weights(const void* q, const float* lse, const attn_kv_cache* cac
  * lens[b] > keep the last `recent` slots stay, and of the others the keep -
  * recent of largest weight (equal weights: the lower slot first; a NaN weight
  * counts as -inf); otherwise every slot stays.  The slots that stay go, in
- * ascending order, to slots 0, 1, ... of `dst` (dst->lens is not used), whose
- * pages must be others than the source's, with their weights:
+ * ascending order, to slots 0, 1, ... of `dst` (dst->lens is not used), with their
+ * weights.  dst's pages must be others than any that the source's tables name for slots
+ * in use: another pool, or free pages of the same one, of the same size and named by
+ * another table (what a page of both holds afterwards is undefined):
  *   kept[b, hk, i]  = source slot of slot i of head hk, -1 behind the last one;
  *   weights_out[b, hk, i] = weights[b, hk, kept], 0 behind the last one;
  *   new_lens[b] = min(lens[b], keep).

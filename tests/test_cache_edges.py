@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from cache_parity import Cache, mask_words, random_tree, tree_ref, weights_ref, within
+from cache_parity import Cache, kept_ref, mask_words, random_tree, tree_ref, weights_ref, within
 from parity import guarded_empty, guards_intact
 
 gpu = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
@@ -309,6 +309,68 @@ def test_weights_with_a_row_that_does_not_exist(dtype, T):
     gone[0, :, 1] = gone[1, :, T - 1] = -math.inf
     ref, tol = weights_ref(q, gone, cache.rows_k, w, [list(range(T))] * 2, [T, T], 0.125)
     within(out, ref, tol, "weights")
+
+
+# ------------------------------------------------- eviction within a pool
+def evict_within(attn, **dst):
+    """Return code of an eviction from k 4096, v 1 << 20 (never dereferenced) on the host."""
+    import ctypes
+
+    size = dict(num_pages=8, page_size=16, max_pages=4)
+    src = attn.KVCache(k=4096, v=1 << 20, block_table=4096, lens=4096, **size)
+    to = attn.KVCache(**{**dict(k=4096, v=1 << 20, block_table=8192, lens=None), **size, **dst})
+    P = ctypes.c_void_p
+    return attn.lib().attn_cache_evict(ctypes.byref(src), P(4096), 64, 8, 2, ctypes.byref(to), P(8192), P(4096), P(8192),
+                                       2, 2, 64, 0, None)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses must not reach a GPU")
+def test_eviction_within_a_pool_is_accepted_by_other_tables():
+    """Accepted: the next answer is that there is no device to run on."""
+    from exact_io_aware_57_b200 import attn
+
+    for dst in (dict(), dict(v=1 << 21), dict(k=8192), dict(block_table=None), dict(k=8192, v=1 << 21, page_size=32)):
+        assert evict_within(attn, **dst) == attn.ATTN_ERR_UNSUPPORTED
+    for dst in (dict(block_table=4096), dict(block_table=4096, v=1 << 21), dict(page_size=32), dict(k=1 << 20, v=8192),
+                dict(k=8192, v=4096)):
+        assert evict_within(attn, **dst) == attn.ATTN_ERR_INVALID
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_evict_into_free_pages_of_the_same_pool(dtype):
+    """There and, with more rows appended, back: the source's old pages are free by then."""
+    from exact_io_aware_57_b200 import attn
+
+    g = torch.Generator().manual_seed(3)
+    lens, keep, recent, page, Hkv, d = [150, 61, 30], 40, 8, 16, 2, 64
+    cache = Cache(lens, Hkv, d, page, dtype, room=8, stale=7.0, spare=12)
+    used = set(cache.table[cache.table >= 0].tolist())
+    free = [p for p in range(cache.k.shape[0]) if p not in used]
+    other = torch.full((3, 4), -9, dtype=torch.int32)
+    for b in range(3):
+        other[b, :4] = torch.tensor(free[4 * b:4 * b + 4])
+    other = other.cuda()
+    k, v, n, table = cache.gpu()
+    keys, vals = [x.clone() for x in cache.rows_k], [x.clone() for x in cache.rows_v]
+    for here, there in ((table, other), (other, table)):
+        w = torch.rand(3, Hkv, 160, generator=g)
+        counts = n.tolist()
+        w_out, kept, n = attn.attn_cache_evict(k, v, w.cuda(), n, keep, k, v, recent=recent, block_table=here,
+                                               out_table=there)
+        status_ok()
+        assert n.tolist() == [min(x, keep) for x in counts]
+        at = there.cpu()
+        for b, m in enumerate(n.tolist()):
+            stay = [kept_ref(w[b, h], counts[b], keep, recent) for h in range(Hkv)]
+            keys[b], vals[b] = (torch.stack([x[b][stay[h], h] for h in range(Hkv)], 1) for x in (keys, vals))
+            for s in range(m):
+                where = int(at[b, s // page]), s % page
+                assert torch.equal(k[where].cpu(), keys[b][s]) and torch.equal(v[where].cpu(), vals[b][s])
+        kn, vn = (torch.randn(3, 8, Hkv, d, generator=g).to(dtype) for _ in range(2))
+        n = attn.attn_cache_append(kn.cuda(), vn.cuda(), k, v, n, block_table=there)
+        keys, vals = [torch.cat([x, kn[b]]) for b, x in enumerate(keys)], [torch.cat([x, vn[b]]) for b, x in enumerate(vals)]
+    status_ok()
 
 
 # ------------------------------------------------- streams of the caller's
