@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpMma) tmem_alloc(&s.tmem_base, kTmemCols);
   if (warp == kWarpLoad && lane == 0) {
     tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_q);
+    if (!p.rows) tma_prefetch_desc(&tm_q);  // (listed rows have no map)
   }
   // columns that no load writes: zeros, so that their scores are finite
   for (int i = threadIdx.x; i < nq * (width - rw.gb * rw.tt) * (D / 8); i += kThreads) {
