@@ -80,21 +80,28 @@ Rows row_tiles(int Hq, int Hkv, int max_rows) {
   return r;
 }
 
-// sum over k < n of floor((a k + b) / m), a, b >= 0 (the lattice points below a
-// line, by the Euclidean reduction of a and m).
-ATTN_DEVINL long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+// Sum of floor((y + KT x) / tt) over x < n: the row tiles wholly before each of n key
+// tiles.  With the whole parts of slope and offset taken out, 0 <= a, b < m, the terms
+// t(x) = floor((a x + b) / m) rise to t = t(n - 1), and summed the other way round,
+//   sum_x t(x) = sum_(1 <= j <= t) #{x < n : a x + b >= j m}
+//              = t n - sum_(0 <= j < t) floor((m j + m - b + a - 1) / a),
+// the same sum with slope and divisor exchanged (the law of reciprocity of such sums:
+// Graham, Knuth, Patashnik, Concrete Mathematics, 3.5): as many turns as Euclid's
+// algorithm takes for KT and tt.  Only the sum passes 32 bits (n < 2^22, y < 2^29).
+ATTN_DEVINL long long tiles_before(unsigned n, unsigned y, unsigned tt) {
   long long sum = 0;
-  while (n) {
-    sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
-    a %= m;
-    b %= m;
-    const unsigned long long top = (unsigned long long)a * n + b;
-    if (top < m) break;
-    n = (unsigned)(top / m);
-    b = (unsigned)(top % m);
-    const unsigned x = m;
-    m = a;
-    a = x;
+  unsigned a = KT, b = y, m = tt;
+  for (int sign = 1; n > 0; sign = -sign) {
+    const unsigned qa = a / m, qb = b / m;
+    a -= qa * m;
+    b -= qb * m;
+    const unsigned t = (a * (n - 1) + b) / m;
+    sum += sign * ((long long)n * (n - 1) / 2 * qa + (long long)n * qb + (long long)n * t);
+    b = m - b + a - 1;
+    n = t;  // 0 where a is
+    const unsigned x = a;
+    a = m;
+    m = x;
   }
   return sum;
 }
@@ -123,7 +130,7 @@ ATTN_DEVINL long long steps_below(const Rows& rw, const Seq& s, int kt) {
   const int shift = s.len - s.cnt;
   const int k0 = shift >= 0 ? shift / KT + 1 : 0;  // the first tile that early rows do not see
   long long cut = 0;
-  if (kt > k0) cut = floor_sum(kt - k0, rw.tt, KT, k0 * KT - shift);
+  if (kt > k0) cut = tiles_before(kt - k0, k0 * KT - shift, rw.tt);
   return ((long long)kt * s.tiles - cut) * rw.gblk + (long long)kt * unit_cost(rw);
 }
 
