@@ -112,12 +112,6 @@ struct BwdParams {
   long long wait_limit;
 };
 
-template <int N>
-ATTN_DEVINL void reg_fence(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 
 // out[tile] += smem tile (fp32), completion tracked by bulk groups
 ATTN_DEVINL void tma_reduce_add_4d(const CUtensorMap* map, const void* src, int c0, int c1, int c2, int c3) {

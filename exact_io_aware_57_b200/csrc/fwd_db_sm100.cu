@@ -88,12 +88,6 @@ struct DBSmem {
   int abort_flag;
 };
 
-template <int N>
-ATTN_DEVINL void reg_fence(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 // Key-tile range of one query tile: 64-key tiles jb .. jb + n - 1 hold every
 // key visible from its rows [mt, min(mt + BM, len_q)), clipped to [k_lo, k_hi).
 struct TileRange {

@@ -114,10 +114,4 @@ struct TreeBoxes {
   }
 };
 
-template <int N>
-ATTN_DEVINL void reg_fence(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 }  // namespace attn

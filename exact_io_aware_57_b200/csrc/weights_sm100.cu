@@ -223,12 +223,6 @@ struct Walk {
   }
 };
 
-template <int N>
-ATTN_DEVINL void reg_fence(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 // Sum of exponentials of N columns of a key, x = s * sc2 + z in pairs (sc2 twice
 // in sc).  EDGE: a column whose row does not see the key, or does not count, adds
 // nothing whatever its score.
