@@ -228,6 +228,44 @@ def test_large_values_after_a_low_first_score(T, Hq, rise):
     within(lse, l_r, tol_l, "lse")
 
 
+# ------------------------------------------------- many new tokens
+@on_gpu
+@pytest.mark.parametrize("T,Hq,Hkv,d,lens,row_lens", [
+    (1000, 4, 2, 128, [300, 0], [1000, 700]),
+    (4096, 1, 1, 64, [77], None),
+    (2049, 2, 1, 64, [128, 1, 500], [2049, 64, 1025]),
+])
+@pytest.mark.parametrize("shape", ["chain", "tree"])
+def test_long_chunks(T, Hq, Hkv, d, lens, row_lens, shape):
+    """A chunk of a prompt, or a tree, of up to the most rows that a call takes."""
+    from exact_io_aware_57_b200 import attn
+
+    g, rng = torch.Generator().manual_seed(T), np.random.default_rng(T)
+    B, counts = len(lens), row_lens or [T] * len(lens)
+    cache = Cache(lens, Hkv, d, 32, BF)
+    q, kn, vn = (torch.randn(B, T, h, d, generator=g).to(BF) for h in (Hq, Hkv, Hkv))
+    for b, r in enumerate(counts):
+        q[b, r:], kn[b, r:], vn[b, r:] = math.nan, math.nan, math.nan
+    see = [random_tree(T, rng) if shape == "tree" else np.tril(np.ones((T, T), dtype=bool)) for _ in range(B)]
+    mask = mask_words(np.stack(see)).cuda() if shape == "tree" else None
+    k, v, cl, table = cache.gpu()
+    ob, o = guarded_empty((B, T, Hq, d), BF)
+    lb, lse = guarded_empty((B, Hq, T), F32)
+    attn.attn_fwd_tree(q.cuda(), k, v, cl, k_new=kn.cuda(), v_new=vn.cuda(), block_table=table, tree_mask=mask,
+                       row_lens=torch.tensor(counts, dtype=torch.int32).cuda(), out=o, lse=lse)
+    status_ok()
+    assert guards_intact(ob) and guards_intact(lb)
+    o_r, l_r, tol_o, tol_l = tree_ref(q, cache.rows_k, cache.rows_v, kn, vn, see, counts, 1 / math.sqrt(d))
+    within(lse, l_r, tol_l, "lse")
+    within(o, o_r, tol_o, "o")
+
+
+@on_gpu
+def test_long_chunk_fp32():
+    q, rows, kn, vn, see, bad = nan_case(700, 2, F32, lens=(100, 0))
+    check_nan(tree_call(q, rows, kn, vn, see), ref_of(q, rows, kn, vn, see), bad)
+
+
 # ------------------------------------------------- largest sizes
 @on_gpu
 @pytest.mark.parametrize("cap", [134215681, 1 << 28])
