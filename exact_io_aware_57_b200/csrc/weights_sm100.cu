@@ -57,7 +57,8 @@ struct WeightsSmem {
   static constexpr int kKeysFew = NT / 3, kKeysMany = 2 * NT / 3;  // nk of the two
   alignas(1024) uint8_t tile[NT][kTileBytes];
   alignas(16) float z[NZ][BR];  // -LSE log2(e); -inf for a row that counts for nothing
-  alignas(16) int last[NZ][BR];  // last slot the row sees
+  alignas(16) int last[NZ][BR];  // last slot the row sees; -1 for a row that counts for nothing
+  int hides[NZ];  // a row that counts has LSE = -inf
   float part[kSums][KT];  // a unit's sums by the warpgroups that do not finish it
   uint64_t t_full[NT], t_empty[NT];
   uint64_t z_full[NZ], z_empty[NZ], s_full[4], s_empty[4];
@@ -492,11 +493,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int zt = i % NZ;
       ok = __all_sync(0xffffffffu, mbar_wait(&s.z_empty[zt], ((i / NZ) & 1) ^ 1, ab));
       if (!ok) return;
+      bool hides = false;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        s.z[zt][v * 32 + lane] = t.lse[v] == -INFINITY || t.last[v] < 0 ? -INFINITY : -t.lse[v] * kLog2e;
-        s.last[zt][v * 32 + lane] = t.last[v];
+        const bool none = t.lse[v] == -INFINITY;
+        hides |= none && t.last[v] >= 0;
+        s.z[zt][v * 32 + lane] = none || t.last[v] < 0 ? -INFINITY : -t.lse[v] * kLog2e;
+        s.last[zt][v * 32 + lane] = none ? -1 : t.last[v];
       }
+      hides = __any_sync(0xffffffffu, hides);
+      if (lane == 0) s.hides[zt] = hides;
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.z_full[zt]);
       ++i;
@@ -580,15 +586,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&s.z_full[zt], (step / NZ) & 1, ab));
           if (!ok) break;
         }
+        const int hides = s.hides[zt];
         ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[wg], (step >> 2) & 1, ab));
         if (!ok) break;
         tc_fence_after();
         const float* z = s.z[zt];
         const int* last = s.last[zt];
-        // rows from i0 on: the tile's last key is hidden from the first of them,
-        // or the last of them do not count
+        // rows from i0 on: the tile's last key is hidden from the first of them, or
+        // some of them count for nothing (q may hold anything there)
         const int i0 = (u.first + j / rw.gblk) * rw.tt;
-        const bool edge = u.kt * KT + KT - 1 > w.s.len - w.s.cnt + i0 || i0 + rw.tt > w.s.cnt || rw.gblk > 1;
+        const bool edge = u.kt * KT + KT - 1 > w.s.len - w.s.cnt + i0 || i0 + rw.tt > w.s.cnt ||
+                          rw.gblk > 1 || hides;
         sum += edge ? add_tile<true>(col, width, z, last, key, sc) : add_tile<false>(col, width, z, last, key, sc);
         tc_fence_before();
         __syncwarp();

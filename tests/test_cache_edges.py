@@ -204,6 +204,37 @@ def test_merge_keeps_nan(dtype):
     assert torch.equal(got[0].transpose(0, 1)[keep], want[0].transpose(0, 1)[keep])
 
 
+@on_gpu
+@pytest.mark.parametrize("lens,T,Hq,Hkv,dtype", [([400, 250], 3, 4, 2, BF), ([700, 300], 200, 6, 2, BF), ([90], 9, 160, 1, BF),
+                                                 ([400, 250], 3, 4, 2, F32), ([130, 200], 60, 4, 2, F32)])
+def test_weights_of_rows_without_a_visible_key(lens, T, Hq, Hkv, dtype):
+    """LSE = -inf: such a row adds nothing, whatever q holds there.  A NaN row or LSE makes
+    the slots that see it NaN."""
+    from exact_io_aware_57_b200 import attn
+
+    g = torch.Generator().manual_seed(6)
+    cache, B = Cache(lens, Hkv, 64, 16, dtype), len(lens)
+    k, _, cl, table = cache.gpu()
+    q = torch.randn(B, T, Hq, 64, generator=g).to(dtype)
+    lse = 6 + torch.rand(B, Hq, T, generator=g)
+    w = torch.rand(B, Hkv, max(lens), generator=g)
+    for b in range(B):
+        for t, x in ((b, math.nan), (T - 1, math.inf)):
+            q[b, t], lse[b, :, t] = x, -math.inf
+    call = lambda: attn.attn_cache_weights(q.cuda(), lse.cuda(), k, cl, w.cuda(), block_table=table,
+                                           out=torch.empty_like(w).cuda()).cpu()
+    out = call()
+    status_ok()
+    ref, tol = weights_ref(q, lse, cache.rows_k, w, [list(range(T))] * B, [T] * B, 0.125)
+    within(out, ref, tol, "weights")
+    lse[0, Hq - 1, 1] = math.nan
+    bad = call()
+    status_ok()
+    seen = torch.zeros_like(w, dtype=torch.bool)
+    seen[0, Hkv - 1, :lens[0] - T + 2] = True
+    assert torch.equal(torch.isnan(bad), seen) and torch.equal(bad[~seen], out[~seen])
+
+
 # ------------------------------------------------- large values
 @on_gpu
 @pytest.mark.parametrize("T,Hq", [(1, 4), (4, 8), (40, 8)])
