@@ -524,8 +524,9 @@ def _used_on(stream, caller, *tensors):
     given out again before what uses them there, and on the stream that was current, has run."""
     if stream is not None:
         for t in tensors:
-            t.record_stream(stream)
-            t.record_stream(caller)
+            if t.is_cuda:  # (what is not is refused with the other arguments)
+                t.record_stream(stream)
+                t.record_stream(caller)
 
 
 def _scratch(workspace, like, dev, size_of, *args):

@@ -540,6 +540,17 @@ def test_memory_of_a_dense_call_on_a_side_stream(name):
     status_ok()
 
 
+@on_gpu
+def test_outputs_on_the_host_are_refused_on_a_side_stream():
+    from exact_io_aware_57_b200 import attn
+
+    k = torch.zeros(1, 8, 2, 64, dtype=BF, device="cuda")
+    q, lens = torch.zeros(1, 1, 2, 64, dtype=BF, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(attn.AttnError, match="out is on cpu"):
+        attn.attn_fwd_tree(q, k, k, lens, out=torch.zeros(1, 1, 2, 64, dtype=BF), stream=torch.cuda.Stream())
+    status_ok()
+
+
 class FakeStream:
     device = torch.device("cuda", 1)
 
