@@ -8,7 +8,9 @@
 // group for P V, the running softmax state (m, l, a) in registers ("Softmax
 // does not need the matrix", "Carry the Normalizer").  The splits' partials are
 // merged by merge.cu.  Splitting strides over tiles, so that splits of ragged
-// sequences stay level without the host knowing a length.
+// sequences stay level without the host knowing a length.  K and V are read again for
+// every 8 rows: 8 sequences of 8191 slots, one token of 32 heads on 8, d = 128 take 316
+// us (bytes once: 83), 4 of 4000 slots with 61 tokens 1.92 ms (8.4 TFLOP/s).
 //
 // Key weights.  A block owns 32 slots of one (sequence, KV head): lane = slot,
 // the warps share out the counted (row, head) pairs, and their sums are added
@@ -126,10 +128,11 @@ __global__ void __launch_bounds__(32 * ROWS) tree_f32_kernel(TreeParams p) {
 // Weights.  A block has 32 slots, a lane each; its warps take AT (row, head)s at a
 // time.  Four in 16 warps, so that a key read from shared memory serves four dot
 // products and four rows' loads are on their way at once: a prompt of 606 tokens of 3
-// heads on one KV head takes 196 us, with one at a time in 8 warps 655.  One in 8 warps
+// heads on one KV head takes 195 us, with one at a time in 8 warps 655 (19 blocks then
+// walk all counted rows each, and 129 SMs have none).  One in 8 warps
 // where these have two rows each at most, as in a decode step, whose time is the
-// latency of a row (4 sequences of 800 .. 1000 slots, 16 heads on 8: 12 us, the other
-// way 29).
+// latency of a row (4 sequences of 800 .. 1000 slots, 16 heads on 8: 10 to 12 us, the
+// other way 29).
 constexpr int weights_warps(int at) { return at == 1 ? 8 : 16; }
 
 template <int D, int AT>

@@ -7,10 +7,13 @@
 // sum stays in a register, and nothing is reduced across threads.  With the LSE
 // at hand there is no running maximum: each score costs one FMA, one
 // exponential and one addition.  A decode step has few rows and is bound by
-// reading K (32 sequences of 8191 slots, 8 KV heads: 72 us for 330 MB); a prompt by
-// the exponentials (16 a cycle and SM against 32 scores of 128-wide dot products on
-// the tensor cores: 8192 tokens of 32 heads in 325 us, 239 of them the exponentials
-// alone).  Measured when that was 341 and not kept: a quarter of the exponentials as polynomials
+// reading K (32 sequences of 1000 .. 8191 slots, 8 KV heads: 73 us for 330 MB).  A
+// prompt's largest share is the exponentials (16 a cycle and SM against 32 scores of
+// 128-wide dot products on the tensor cores), but they do not bound it by themselves:
+// 8192 tokens of 32 heads take 326 us, 239 if their unit never stood still, and 285
+// with no exponential at all (of the state that took 341; 313 with one MMA of eight,
+// 266 with neither): what is left is a step's hand-overs between the tensor cores and
+// the warpgroup that owns its one score buffer.  Measured at 341 and not kept: a quarter of the exponentials as polynomials
 // (355 us: four warps per scheduler do not hide their chains), two issuing threads
 // (357: 80 registers a thread, spills), each Q tile kept for two key tiles (341).
 //
